@@ -10,7 +10,7 @@
  *
  * Conventions shared by every entry point
  *  - Pointers named in a signature are DEVICE pointers unless stated, and
- *    must be 16-byte aligned.  Matrices are row-major; weights use the
+ *    must be 16-byte aligned unless a call asks for less (workspaces always).  Matrices are row-major; weights use the
  *    [out][in] layout, stacked per expert.
  *  - Every call is asynchronous on `stream` (a hipStream_t; NULL = the null
  *    stream).  The library never allocates device memory, never synchronises
@@ -134,7 +134,8 @@ typedef struct {
 const char* moe_status_str(moe_status s);
 
 /* Workspace needed by an entry point: which = 0 moe_layer_forward,
- * 1 moe_permute, 2 moe_expert_ffn, 3 moe_shared_ffn, 4 moe_layer_backward.
+ * 1 moe_permute, 2 moe_expert_ffn, 3 moe_shared_ffn, 4 moe_layer_backward,
+ * 5 moe_sort_tokens (only T, d, E and k are read, within that call's limits).
  * Writes the byte count to *bytes (host pointer).  Pure host computation. */
 moe_status moe_workspace_bytes(const moe_dims* dims, moe_prec prec, int which, size_t* bytes);
 
@@ -379,6 +380,129 @@ moe_status moe_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint
  * n = 0 is a no-op; EINVAL for n < 0 or above INT32_MAX, a null pointer, or
  * a or b not 16-byte aligned. */
 moe_status moe_bf16_mma_tiles(const void* a, const void* b, const float* c, float* d, int64_t n, void* stream);
+
+/* ---- Routed tokens sorted by expert and back, with absent routes ----------
+ * moe_permute and moe_combine for callers whose routes may be absent, with
+ * the gradients of both: a route whose expert id lies outside [0, E) is
+ * absent (a padding token, a dropped route, an expert of another rank, whose
+ * ids become local by subtracting the rank's first expert).  Of `dims` only
+ * T, d, k and, in moe_sort_tokens, E are read: T <= 4,194,303, any d >= 1,
+ * 1 <= k <= 16 (k may exceed E), E <= 1024.  MOE_F32 and MOE_BF16; rows need
+ * element alignment only.  Indices are int32.  Outputs must not overlap
+ * inputs, except that y may be y_add and dx may be dx_add.
+ *
+ * moe_sort_tokens: the present routes in (token, slot) order, grouped by
+ * expert (blog post, "Choosing the right communication direction /
+ * Scheduling"); the same expert twice in a token's ids gives two rows.
+ *   expert_counts [E], expert_offsets [E+1] (offsets[E] = present routes),
+ *   token_row [T][k]: the route's row, -1 if absent,
+ *   row_token [T*k]: the row's token, x_perm [T*k][d]: x[row_token[row]];
+ *   entries from row offsets[E] on are left as they were.
+ *   x_perm may be NULL (schedule only).  ws: moe_workspace_bytes(which=5). */
+moe_status moe_sort_tokens(const moe_dims* dims, moe_prec prec, const int32_t* topk_idx, const void* x,
+                           int32_t* expert_counts, int32_t* expert_offsets, int32_t* row_token, int32_t* token_row,
+                           void* x_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of x_perm with respect to x:
+ *   dx[t] = sum_{j present} dx_perm[token_row[t][j]] + dx_add[t],
+ * fp32 in slot order, rounded once.  dx_add may be NULL.  A token_row entry
+ * outside [0, T*k) is an absent route, here and below. */
+moe_status moe_sort_tokens_backward(const moe_dims* dims, moe_prec prec, const void* dx_perm, const int32_t* token_row,
+                                    const void* dx_add, void* dx, void* stream);
+
+/* The weighted sum back to token order (blog post footnote to "Overlapping
+ * computation and communication in MoE"):
+ *   y[t] = sum_{j present} topk_w[t][j] * o_perm[token_row[t][j]] + y_add[t],
+ * fp32 in slot order, rounded once; a token without routes gets y_add, or 0.
+ * y_add may be NULL.  Weights and rows of absent routes are not read. */
+moe_status moe_unsort_tokens(const moe_dims* dims, moe_prec prec, const void* o_perm, const int32_t* token_row,
+                             const float* topk_w, const void* y_add, void* y, void* stream);
+
+/* Gradients of moe_unsort_tokens for dy (that of y_add is dy itself):
+ *   do_perm[token_row[t][j]] = topk_w[t][j] * dy[t]; rows of no route are
+ *     left as they were;
+ *   dtopk_w[t][j] = <dy[t], o_perm[token_row[t][j]]> in fp32, 0 for an absent
+ *     route.
+ * Either output may be NULL, and with it what it alone needs (topk_w for
+ * do_perm, o_perm for dtopk_w). */
+moe_status moe_unsort_tokens_backward(const moe_dims* dims, moe_prec prec, const void* dy, const void* o_perm,
+                                      const int32_t* token_row, const float* topk_w, void* do_perm, float* dtopk_w,
+                                      void* stream);
+
+/* ---- Norms before and after a residual block ------------------------------
+ * Host struct of the step between two blocks: residual x [T][d] and a block's
+ * output y [T][d] in, next residual x' and next block's input a out.  With
+ * r(v) = 1 / sqrt(mean(v^2) + eps) per token and g = t / gate_every:
+ *   n  = y r(y) w_post  (post_norm; w_post NULL: ones), else n = y
+ *   x' = alpha x + beta gate[g] n           (gate NULL: ones)
+ *   a  = x' r(x') w_pre                     (w_pre NULL: ones)
+ * Activations (y, a and their gradients) are of type `prec`, MOE_F32 or
+ * MOE_BF16; the residual (x, x' and their gradients) too, or fp32 with
+ * res_f32.  w_post, w_pre [d] and gate [ceil(T / gate_every)][d] are fp32: one
+ * gate row for every gate_every consecutive tokens (T: one for all).
+ * T <= 4,194,303, 1 <= d <= 16384, eps > 0; rows need element alignment only.
+ * fp32 arithmetic, every output rounded once (a from the unrounded x'). */
+typedef struct {
+  int64_t T;
+  int64_t gate_every;     /* read only with a gate */
+  int32_t d;
+  int32_t res_f32;
+  int32_t post_norm;
+  float alpha, beta, eps;
+} moe_block;
+
+/* Forward.  y NULL: only a = norm of x (x_out and gate NULL, post_norm 0; the
+ * step before the first block).  a NULL: only x' (w_pre NULL; after the last
+ * block).  r_post and r_pre [T] fp32 keep r(y) and r(x') for the backward; may
+ * be NULL.  x_out may be x; outputs must not overlap inputs otherwise. */
+moe_status moe_block_norm(const moe_block* block, moe_prec prec, const void* x, const void* y, const float* w_post,
+                          const float* gate, const float* w_pre, void* x_out, void* a, float* r_post, float* r_pre,
+                          void* stream);
+
+/* Backward from the gradients of x' (dx_out) and a (da), either NULL where
+ * there is none, the forward's x', y, r_post and r_pre:
+ *   xh = x' r_pre, u = da w_pre, dz = dx_out + r_pre (u - xh mean(u xh))
+ *   dx = alpha dz (dz without a block output), dw_pre = sum_t da xh
+ *   e = beta dz, dn = e gate, dgate[g] = sum over its tokens of e n
+ *   yh = y r_post, v = dn w_post, dw_post = sum_t dn yh
+ *   dy = r_post (v - yh mean(v yh))  (post_norm), else dn.
+ * Without a block output y and dy are NULL (then x_out is the forward's x).
+ * dw_post, dgate, dw_pre (fp32) may be NULL, and need their w_post, gate,
+ * w_pre.  An empty batch gives zero dw_post and dw_pre.  Outputs must not
+ * overlap inputs.  ws: moe_block_norm_scratch_bytes(T, d) bytes (0 for sizes
+ * outside the limits). */
+size_t moe_block_norm_scratch_bytes(int64_t T, int32_t d);
+moe_status moe_block_norm_backward(const moe_block* block, moe_prec prec, const void* dx_out, const void* da,
+                                   const void* x_out, const void* y, const float* r_post, const float* r_pre,
+                                   const float* w_post, const float* gate, const float* w_pre, void* dx, void* dy,
+                                   float* dw_post, float* dgate, float* dw_pre, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* ---- Gradient norm and clipping -------------------------------------------
+ * n tensors: grads (HOST array of device pointers), numel (HOST array of
+ * element counts), types (HOST array: MOE_F32 or MOE_BF16 each).  Pointers need
+ * element alignment; a tensor of no elements may be NULL.  The host arrays
+ * are read before the call returns.  Non-finite gradients are allowed here.
+ *
+ * moe_grad_norm: *norm (device, fp32) = sqrt(sum of all squares), summed in
+ * fp64 in an order fixed by the sizes, rounded once.
+ * ws: moe_grad_norm_scratch_bytes(numel, n). */
+size_t moe_grad_norm_scratch_bytes(const int64_t* numel, int32_t n);
+moe_status moe_grad_norm(const void* const* grads, const int64_t* numel, const int32_t* types, int32_t n, float* norm,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), fp32 product rounded
+ * once; out (HOST array of device pointers) may hold the tensors of grads
+ * themselves (in place) or others of the same types; no tensor of out may
+ * otherwise overlap another of either list.  norm_in (device, fp32): the norm
+ * to clip by, for instance one joined over ranks; norm and ws are then unused.
+ * norm_in NULL: the norm of these tensors, left in *norm, the same bits as
+ * moe_grad_norm's.  A NaN norm gives NaN, an infinite one zeros (NaN where a
+ * gradient is not finite).  max_norm: finite, >= 0.
+ * ws: moe_grad_norm_scratch_bytes(numel, n). */
+moe_status moe_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* types,
+                          int32_t n, float max_norm, const float* norm_in, float* norm, void* ws, size_t ws_bytes,
+                          void* stream);
 
 #ifdef __cplusplus
 }

@@ -45,8 +45,15 @@ class moe_routing(ctypes.Structure):
         "gu_shared")]
 
 
+class moe_block(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("gate_every", ctypes.c_int64), ("d", ctypes.c_int32),
+                ("res_f32", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _DIMS = ctypes.POINTER(moe_dims)
+_BLOCK = ctypes.POINTER(moe_block)
 _SIGS = {
     "moe_status_str": ([ctypes.c_int], ctypes.c_char_p),
     "moe_workspace_bytes": ([_DIMS, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
@@ -74,6 +81,17 @@ _SIGS = {
     "moe_quantize_mxfp8_rows_t": ([_P, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, ctypes.c_int32, ctypes.c_int64,
                                    _P, _P, _P], ctypes.c_int),
     "moe_mx_mma_tiles": ([_P, _P, _P, _P, _P, _P, ctypes.c_int64, _P], ctypes.c_int),
+    "moe_sort_tokens": ([_DIMS, ctypes.c_int] + [_P] * 8 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_sort_tokens_backward": ([_DIMS, ctypes.c_int] + [_P] * 5, ctypes.c_int),
+    "moe_unsort_tokens": ([_DIMS, ctypes.c_int] + [_P] * 6, ctypes.c_int),
+    "moe_unsort_tokens_backward": ([_DIMS, ctypes.c_int] + [_P] * 7, ctypes.c_int),
+    "moe_block_norm": ([_BLOCK, ctypes.c_int] + [_P] * 10, ctypes.c_int),
+    "moe_block_norm_scratch_bytes": ([ctypes.c_int64, ctypes.c_int32], ctypes.c_size_t),
+    "moe_block_norm_backward": ([_BLOCK, ctypes.c_int] + [_P] * 15 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_grad_norm_scratch_bytes": ([_P, ctypes.c_int32], ctypes.c_size_t),
+    "moe_grad_norm": ([_P, _P, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_clip_grads": ([_P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P],
+                       ctypes.c_int),
     "moe_bf16_mma_tiles": ([_P, _P, _P, _P, ctypes.c_int64, _P], ctypes.c_int),
 }
 

@@ -1,0 +1,349 @@
+"""Torch-facing wrappers of the operators around the layer: routed tokens
+sorted by expert and back, the norms before and after a residual block, and
+gradient clipping.  They check their tensors, allocate outputs and workspaces
+with torch and pass pointers and the stream that is current on the tensors'
+device; no arithmetic happens here."""
+import array
+import contextlib
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib
+from ._lib import PREC, call, moe_block
+from .ops import Dims
+
+_ACT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _act(prec):
+    if prec not in _ACT:
+        raise ValueError("prec must be 'f32' or 'bf16', not %r" % (prec,))
+    return _ACT[prec]
+
+
+def _check(name, t, dtype, shape, device):
+    """t as a device pointer; raises unless it is a contiguous tensor of this
+    type and shape on this device.  None: a null pointer."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s" % (
+            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+            "" if t.is_contiguous() else " (not contiguous)"))
+    return t.data_ptr()
+
+
+def _need(name, t):
+    if t is None:
+        raise ValueError("%s is missing" % name)
+    if t.device.type != "cuda":
+        raise ValueError("%s must be on a GPU, not on %s" % (name, t.device))
+    return t.device
+
+
+def _on(device):
+    """Makes `device` current around a launch (its streams, its kernels)."""
+    if torch.cuda.current_device() == device.index:
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _device(device):
+    d = torch.device(device)
+    return torch.device(d.type, torch.cuda.current_device()) if d.type == "cuda" and d.index is None else d
+
+
+# ---- routed tokens sorted by expert and back -------------------------------
+class SortPlan:
+    """Outputs and workspace of moe_sort_tokens for one configuration, so that
+    repeated calls allocate nothing.  x_perm and row_token may be the
+    caller's; their entries from row offsets[E] on are never written.
+    gather=False: the schedule alone, no x_perm."""
+
+    def __init__(self, dims: Dims, prec: str, device="cuda", x_perm=None, row_token=None, gather=True):
+        act = _act(prec)
+        n = ctypes.c_size_t(0)
+        self.dims, self.prec = dims, prec
+        self.cdims = dims.c()
+        call("moe_workspace_bytes", ctypes.byref(self.cdims), PREC[prec], 5, ctypes.byref(n))
+        self.device = dev = _device(x_perm.device if x_perm is not None else
+                                    row_token.device if row_token is not None else device)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.counts = torch.empty(dims.E, **i32)
+        self.offsets = torch.empty(dims.E + 1, **i32)
+        self.token_row = torch.empty(dims.T, dims.k, **i32)
+        self.row_token = torch.empty(dims.R, **i32) if row_token is None else row_token
+        self.x_perm = torch.empty(dims.R, dims.d, dtype=act, device=dev) if x_perm is None and gather else x_perm
+        _check("row_token", self.row_token, torch.int32, (dims.R,), dev)
+        _check("x_perm", self.x_perm, act, (dims.R, dims.d), dev)
+        self.ws_bytes = n.value
+        self.ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device=dev)
+
+    def run(self, topk_idx, x=None):
+        """(counts, offsets, row_token, token_row, x_perm) of the ids topk_idx
+        [T][k] int32 and the tokens x [T][d]."""
+        D, dev = self.dims, self.device
+        if self.x_perm is not None:
+            _need("x", x)
+        _need("topk_idx", topk_idx)
+        idx = _check("topk_idx", topk_idx, torch.int32, (D.T, D.k), dev)
+        xp = _check("x", x, _ACT[self.prec], (D.T, D.d), dev)
+        with _on(dev):
+            call("moe_sort_tokens", self.cdims, PREC[self.prec], idx, xp, self.counts.data_ptr(),
+                 self.offsets.data_ptr(), self.row_token.data_ptr(), self.token_row.data_ptr(),
+                 None if self.x_perm is None else self.x_perm.data_ptr(), self.ws.data_ptr(), self.ws_bytes,
+                 _stream(dev))
+        return self.counts, self.offsets, self.row_token, self.token_row, self.x_perm
+
+
+def sort_tokens(topk_idx, x, dims: Dims, prec: str, gather=True):
+    """moe_sort_tokens into fresh tensors: (counts, offsets, row_token,
+    token_row, x_perm).  row_token and x_perm hold nothing of use from row
+    offsets[E] on."""
+    return SortPlan(dims, prec, _need("topk_idx", topk_idx), gather=gather).run(topk_idx, x)
+
+
+def sort_tokens_backward(dx_perm, token_row, dx_add, dims: Dims, prec: str, dx=None):
+    """moe_sort_tokens_backward: dx [T][d] from dx_perm [T*k][d]; dx_add [T][d]
+    or None is added.  dx: the output tensor, which may be dx_add."""
+    act, dev = _act(prec), _need("dx_perm", dx_perm)
+    if dx is None:
+        dx = torch.empty(dims.T, dims.d, dtype=act, device=dev)
+    args = (_check("dx_perm", dx_perm, act, (dims.R, dims.d), dev),
+            _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
+            _check("dx_add", dx_add, act, (dims.T, dims.d), dev), _check("dx", dx, act, (dims.T, dims.d), dev))
+    with _on(dev):
+        call("moe_sort_tokens_backward", dims.c(), PREC[prec], *args, _stream(dev))
+    return dx
+
+
+def unsort_tokens(o_perm, token_row, topk_w, y_add, dims: Dims, prec: str, y=None):
+    """moe_unsort_tokens: the weighted sum y [T][d] of o_perm's rows, y_add
+    [T][d] or None added.  y: the output tensor, which may be y_add."""
+    act, dev = _act(prec), _need("o_perm", o_perm)
+    if y is None:
+        y = torch.empty(dims.T, dims.d, dtype=act, device=dev)
+    args = (_check("o_perm", o_perm, act, (dims.R, dims.d), dev),
+            _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
+            _check("topk_w", topk_w, torch.float32, (dims.T, dims.k), dev),
+            _check("y_add", y_add, act, (dims.T, dims.d), dev), _check("y", y, act, (dims.T, dims.d), dev))
+    with _on(dev):
+        call("moe_unsort_tokens", dims.c(), PREC[prec], *args, _stream(dev))
+    return y
+
+
+def unsort_tokens_backward(dy, o_perm, token_row, topk_w, dims: Dims, prec: str, do_perm=None, need_do=True,
+                           need_dw=True):
+    """moe_unsort_tokens_backward: (do_perm [T*k][d], dtopk_w [T][k] fp32), None
+    for one that is not needed.  do_perm: the output tensor; rows of no route
+    are left as they were (a fresh tensor holds nothing of use there)."""
+    act, dev = _act(prec), _need("dy", dy)
+    if do_perm is None and need_do:
+        do_perm = torch.empty(dims.R, dims.d, dtype=act, device=dev)
+    if not need_do:
+        do_perm = None
+    dw = torch.empty(dims.T, dims.k, dtype=torch.float32, device=dev) if need_dw else None
+    args = (_check("dy", dy, act, (dims.T, dims.d), dev), _check("o_perm", o_perm, act, (dims.R, dims.d), dev),
+            _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
+            _check("topk_w", topk_w, torch.float32, (dims.T, dims.k), dev),
+            _check("do_perm", do_perm, act, (dims.R, dims.d), dev), None if dw is None else dw.data_ptr())
+    with _on(dev):
+        call("moe_unsort_tokens_backward", dims.c(), PREC[prec], *args, _stream(dev))
+    return do_perm, dw
+
+
+# ---- norms before and after a residual block -------------------------------
+@dataclass(frozen=True)
+class Block:
+    """The step between two blocks (moe_block): T tokens of d channels, prec of
+    the activations, res_f32 an fp32 residual, post_norm a norm of the block's
+    output, alpha and beta the scales of residual and output, gate_every the
+    tokens per gate row (0: one row for all)."""
+    T: int
+    d: int
+    prec: str = "bf16"
+    res_f32: bool = False
+    post_norm: bool = False
+    alpha: float = 1.0
+    beta: float = 1.0
+    eps: float = 1e-6
+    gate_every: int = 0
+
+    @property
+    def every(self):
+        return self.gate_every or max(self.T, 1)
+
+    @property
+    def gates(self):
+        """Rows of the gate."""
+        return (self.T + self.every - 1) // self.every if self.gate_every else 1
+
+    @property
+    def act(self):
+        return _act(self.prec)
+
+    @property
+    def res(self):
+        return torch.float32 if self.res_f32 else self.act
+
+    def c(self):
+        return moe_block(self.T, self.every, self.d, self.res_f32, self.post_norm, self.alpha, self.beta, self.eps)
+
+    def vectors(self, w_pre, w_post, gate, dev):
+        f32 = torch.float32
+        return (_check("w_post", w_post, f32, (self.d,), dev), _check("gate", gate, f32, (self.gates, self.d), dev),
+                _check("w_pre", w_pre, f32, (self.d,), dev))
+
+
+class BlockNormPlan:
+    """Outputs of moe_block_norm for one configuration: x_out [T][d] (None
+    without a block output), a [T][d] (None with pre_norm=False), r_post and
+    r_pre [T] for the backward."""
+
+    def __init__(self, block: Block, device="cuda", pre_norm=True):
+        self.block, self.device = block, _device(device)
+        self.cblock = block.c()
+        T, d, dev = block.T, block.d, self.device
+        self.x_out = torch.empty(T, d, dtype=block.res, device=dev)
+        self.a = torch.empty(T, d, dtype=block.act, device=dev) if pre_norm else None
+        self.r_pre = torch.empty(T, dtype=torch.float32, device=dev) if pre_norm else None
+        self.r_post = torch.empty(T, dtype=torch.float32, device=dev) if block.post_norm else None
+
+    def run(self, x, y=None, w_pre=None, w_post=None, gate=None):
+        """(x_out, a); x_out is x itself where there is no block output y."""
+        b, dev = self.block, self.device
+        _need("x", x)
+        px = _check("x", x, b.res, (b.T, b.d), dev)
+        py = _check("y", y, b.act, (b.T, b.d), dev)
+        wp, g, w = b.vectors(w_pre, w_post, gate, dev)
+        with _on(dev):
+            call("moe_block_norm", self.cblock, PREC[b.prec], px, py, wp, g, w,
+                 None if y is None else self.x_out.data_ptr(), None if self.a is None else self.a.data_ptr(),
+                 None if self.r_post is None else self.r_post.data_ptr(),
+                 None if self.r_pre is None else self.r_pre.data_ptr(), _stream(dev))
+        return (x if y is None else self.x_out), self.a
+
+
+def block_norm(block: Block, x, y=None, w_pre=None, w_post=None, gate=None, pre_norm=True):
+    """moe_block_norm into fresh tensors: (x_out, a, plan); the plan keeps
+    r_pre and r_post for block_norm_backward."""
+    plan = BlockNormPlan(block, _need("x", x), pre_norm)
+    return plan.run(x, y, w_pre, w_post, gate) + (plan,)
+
+
+class BlockNormBackwardPlan:
+    """Gradients and workspace of moe_block_norm_backward for one
+    configuration: dx and dy [T][d], grads of the weights that are given (fp32
+    dw_pre, dw_post [d], dgate [gates][d])."""
+
+    def __init__(self, block: Block, device="cuda", w_pre=True, w_post=True, gate=False, output=True):
+        """output=False: a step without a block output (no dy)."""
+        self.block, self.device = block, _device(device)
+        self.cblock = block.c()
+        T, d, dev = block.T, block.d, self.device
+        self.dx = torch.empty(T, d, dtype=block.res, device=dev)
+        self.dy = torch.empty(T, d, dtype=block.act, device=dev) if output else None
+        self.grads = {}
+        if w_pre:
+            self.grads["dw_pre"] = torch.empty(d, dtype=torch.float32, device=dev)
+        if w_post and block.post_norm:
+            self.grads["dw_post"] = torch.empty(d, dtype=torch.float32, device=dev)
+        if gate:
+            self.grads["dgate"] = torch.empty(block.gates, d, dtype=torch.float32, device=dev)
+        self.ws_bytes = _lib.lib().moe_block_norm_scratch_bytes(T, d)
+        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=dev)
+
+    def run(self, dx_out, da, x_out, y, r_pre, r_post, w_pre=None, w_post=None, gate=None):
+        """(dx, dy, grads) from the gradients of x_out and a (None: no
+        gradient), the forward's x_out, y and row statistics."""
+        b, dev = self.block, self.device
+        _need("dx_out or da", da if dx_out is None else dx_out)
+        rows, f32 = (b.T, b.d), torch.float32
+        args = (_check("dx_out", dx_out, b.res, rows, dev), _check("da", da, b.act, rows, dev),
+                _check("x_out", x_out, b.res, rows, dev), _check("y", y, b.act, rows, dev),
+                _check("r_post", r_post, f32, (b.T,), dev), _check("r_pre", r_pre, f32, (b.T,), dev))
+        vec = b.vectors(w_pre, w_post, gate, dev)
+        g = {n: t.data_ptr() for n, t in self.grads.items()}
+        with _on(dev):
+            call("moe_block_norm_backward", self.cblock, PREC[b.prec], *args, *vec, self.dx.data_ptr(),
+                 None if self.dy is None else self.dy.data_ptr(), g.get("dw_post"), g.get("dgate"), g.get("dw_pre"),
+                 self.ws.data_ptr(), self.ws_bytes, _stream(dev))
+        return self.dx, self.dy, self.grads
+
+
+def block_norm_backward(block: Block, dx_out, da, x_out, y, r_pre, r_post, w_pre=None, w_post=None, gate=None):
+    """moe_block_norm_backward into fresh tensors: (dx, dy, grads), grads of
+    every weight that is given."""
+    plan = BlockNormBackwardPlan(block, _need("dx_out or da", da if dx_out is None else dx_out), w_pre is not None,
+                                 w_post is not None, gate is not None, y is not None)
+    return plan.run(dx_out, da, x_out, y, r_pre, r_post, w_pre, w_post, gate)
+
+
+# ---- gradient norm and clipping --------------------------------------------
+_TYPE = {torch.float32: PREC["f32"], torch.bfloat16: PREC["bf16"]}
+
+
+def _tensors(name, tensors):
+    """Host arrays (addresses, element counts, types) of a list of tensors."""
+    ptrs, numel, types = array.array("Q"), array.array("q"), array.array("i")
+    device = None
+    for i, t in enumerate(tensors):
+        if t.dtype not in _TYPE or not t.is_contiguous() or t.device != (device or _need(name, t)):
+            raise ValueError("%s[%d] must be a contiguous bf16 or fp32 tensor on the device of the others" % (name, i))
+        device = t.device
+        ptrs.append(t.data_ptr())
+        numel.append(t.numel())
+        types.append(_TYPE[t.dtype])
+    return ptrs, numel, types, device
+
+
+def _scratch(numel, device):
+    n = _lib.lib().moe_grad_norm_scratch_bytes(numel.buffer_info()[0], len(numel))
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
+
+
+def grad_norm(grads):
+    """moe_grad_norm: the norm over all tensors, fp32 [1] on their device."""
+    ptrs, numel, types, dev = _tensors("grads", grads)
+    if dev is None:
+        raise ValueError("grads holds no tensor")
+    norm = torch.empty(1, dtype=torch.float32, device=dev)
+    ws, n = _scratch(numel, dev)
+    with _on(dev):
+        call("moe_grad_norm", ptrs.buffer_info()[0], numel.buffer_info()[0], types.buffer_info()[0], len(ptrs),
+             norm.data_ptr(), ws.data_ptr(), n, _stream(dev))
+    return norm
+
+
+def clip_grads(grads, max_norm, norm=None, out=None):
+    """moe_clip_grads: scales the gradients to a global norm of at most
+    max_norm, in place or into the tensors `out`; returns (out, norm).  norm
+    (fp32 [1]): the norm to clip by, for instance one joined over ranks; None:
+    that of these tensors."""
+    ptrs, numel, types, dev = _tensors("grads", grads)
+    if dev is None:
+        raise ValueError("grads holds no tensor")
+    optrs = ptrs
+    if out is not None:
+        optrs, onumel, otypes, odev = _tensors("out", out)
+        if onumel != numel or otypes != types or odev != dev:
+            raise ValueError("out must match grads in number, size, type and device")
+    if len({p for p, n in zip(optrs, numel) if n}) != sum(1 for n in numel if n):
+        raise ValueError("a tensor would be scaled twice: %s holds one more than once" % ("grads" if out is None
+                                                                                         else "out"))
+    given = _check("norm", norm, torch.float32, (1,), dev)
+    ws, n, ws_ptr = None, 0, None
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        ws, n = _scratch(numel, dev)
+        ws_ptr = ws.data_ptr()
+    with _on(dev):
+        call("moe_clip_grads", ptrs.buffer_info()[0], optrs.buffer_info()[0], numel.buffer_info()[0],
+             types.buffer_info()[0], len(ptrs), max_norm, given, norm.data_ptr(), ws_ptr, n, _stream(dev))
+    return (grads if out is None else out), norm

@@ -676,6 +676,7 @@ const char* moe_status_str(moe_status s) {
 }
 
 moe_status moe_workspace_bytes(const moe_dims* dims, moe_prec prec, int which, size_t* bytes) {
+  if (which == 5 && bytes) return sort_workspace_bytes(dims, prec, bytes);
   MOE_TRY(check_dims(dims, prec));
   if (!bytes || which < 0 || which > 4) return MOE_EINVAL;
   *bytes = workspace_size(dims, prec, which);

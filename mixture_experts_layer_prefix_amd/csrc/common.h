@@ -244,6 +244,20 @@ hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t s);
 hipError_t launch_combine(bool act_f32, const void* o_perm, const int32_t* token_row, const float* topk_w,
                           const void* y_shared, void* y, int64_t T, int d, int k, hipStream_t s);
 
+// moe_workspace_bytes, which = 5 (api_block.cpp).
+moe_status sort_workspace_bytes(const moe_dims* dims, moe_prec prec, size_t* bytes);
+
+// Tokens sorted by expert and back with absent routes (sort.hip).  w null:
+// every weight 1; add null: nothing added; do_perm or dw null: not computed.
+size_t sort_scratch_bytes(int64_t T, int k, int E);
+hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k,
+                       int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm,
+                       void* scratch, hipStream_t s);
+hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, const float* w, const void* add, void* y,
+                         int64_t T, int d, int k, hipStream_t s);
+hipError_t launch_unsort_bwd(bool f32, const void* dy, const void* o_perm, const int32_t* token_row, const float* w,
+                             void* do_perm, float* dw, int64_t T, int d, int k, hipStream_t s);
+
 // Backward helpers.  Padded row capacity of a K-grouped operand: every
 // group's rows rounded up to `pad` (a multiple of 64).
 int64_t bwd_padded_rows(int64_t rows, int groups, int pad);

@@ -1,0 +1,284 @@
+// Tokens sorted by expert and back, with the gradients of both, for routes
+// that may be absent (an expert id outside [0, E): a padding token, a dropped
+// route, an expert of another rank) and rows of any length.
+//
+// Route r = t * k + j goes to expert e = topk_idx[t][j].  Its row is
+// offsets[e] plus the number of present routes of e with a smaller r, so an
+// expert's rows follow in (token, slot) order; absent routes get row -1.
+//   sort             x_perm[row] = x[t]
+//   sort backward    dx[t] = sum_j dx_perm[row_j] (+ dx_add[t])
+//   unsort           y[t] = sum_j w_j o_perm[row_j] (+ y_add[t])
+//   unsort backward  do_perm[row_j] = w_j dy[t], dw_j = <dy[t], o_perm[row_j]>
+// with j over the present routes in slot order, fp32 sums and one rounding.
+// Every one of them is a single pass over the rows, bound by memory.
+#include "rows.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kSortRoutes = 256;  // routes per schedule workgroup, one per thread
+
+// Routes per expert of each workgroup's 256 routes, expert-major.
+__global__ void __launch_bounds__(kSortRoutes) sort_count_kernel(const int32_t* __restrict__ idx, int64_t R, int E,
+                                                                 int32_t* __restrict__ block_counts) {
+  __shared__ int32_t h[1024];
+  for (int e = threadIdx.x; e < E; e += kSortRoutes) h[e] = 0;
+  __syncthreads();
+  const int64_t r = (int64_t)blockIdx.x * kSortRoutes + threadIdx.x;
+  const int e = r < R ? idx[r] : -1;
+  if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += kSortRoutes) block_counts[(int64_t)i * gridDim.x + blockIdx.x] = h[i];
+}
+
+// Exclusive prefix over the threads of a 256-thread workgroup; *total its sum.
+__device__ __forceinline__ int scan256(int v, int* lds, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 63) lds[wave] = inc;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) before += lds[w];
+    all += lds[w];
+  }
+  *total = all;
+  return before + inc - v;
+}
+
+// One workgroup per expert: its column of block counts becomes prefixes.
+__global__ void __launch_bounds__(256) sort_scan_kernel(int32_t* __restrict__ block_counts, int nb,
+                                                        int32_t* __restrict__ counts) {
+  __shared__ int lds[4];
+  int32_t* col = block_counts + (int64_t)blockIdx.x * nb;
+  const int per = (nb + 255) / 256;
+  const int b0 = min((int)threadIdx.x * per, nb), b1 = min(b0 + per, nb);
+  int sum = 0, total;
+  for (int b = b0; b < b1; ++b) sum += col[b];
+  int run = scan256(sum, lds, &total);
+  for (int b = b0; b < b1; ++b) {
+    const int c = col[b];
+    col[b] = run;
+    run += c;
+  }
+  if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// Lanes of the wave that hold the same id (ids below 1024; lanes with a
+// negative id get an empty mask): one ballot per bit of the id.
+__device__ __forceinline__ uint64_t same_id_lanes(int e) {
+  uint64_t m = __ballot(e >= 0);
+#pragma unroll
+  for (int bit = 0; bit < 10; ++bit) {
+    const uint64_t b = __ballot((e >> bit) & 1);
+    m &= ((e >> bit) & 1) ? b : ~b;
+  }
+  return e >= 0 ? m : 0;
+}
+
+__global__ void __launch_bounds__(kSortRoutes) sort_rank_kernel(const int32_t* __restrict__ idx, int64_t R, int E, int k,
+                                                                const int32_t* __restrict__ block_base,
+                                                                const int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ row_token,
+                                                                int32_t* __restrict__ token_row) {
+  __shared__ int32_t cursor[1024];
+  __shared__ int lds[4];
+  // offsets: four consecutive experts per thread
+  const int e0 = threadIdx.x * 4;
+  int c[4], sum = 0, total;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    c[q] = e0 + q < E ? counts[e0 + q] : 0;
+    sum += c[q];
+  }
+  int run = scan256(sum, lds, &total);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (e0 + q < E) {
+      cursor[e0 + q] = run + block_base[(int64_t)(e0 + q) * gridDim.x + blockIdx.x];
+      if (blockIdx.x == 0) offsets[e0 + q] = run;
+    }
+    run += c[q];
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) offsets[E] = total;
+  const int64_t r = (int64_t)blockIdx.x * kSortRoutes + threadIdx.x;
+  int e = r < R ? idx[r] : -1;
+  if ((unsigned)e >= (unsigned)E) e = -1;
+  const uint64_t same = same_id_lanes(e);
+  const int lane = threadIdx.x & 63;
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  // the four waves take their rows in turn
+  int row = -1;
+  for (int w = 0; w < kSortRoutes / 64; ++w) {
+    __syncthreads();
+    if ((threadIdx.x >> 6) == w && e >= 0) {
+      row = cursor[e] + rank;
+      if ((same >> lane) == 1) cursor[e] += __popcll(same);  // the id's last lane; the wave has read
+    }
+  }
+  if (r < R) {
+    token_row[r] = row;
+    if (row >= 0) row_token[row] = (int32_t)(r / k);
+  }
+}
+
+__global__ void __launch_bounds__(256) sort_empty_kernel(int32_t* counts, int32_t* offsets, int E) {
+  for (int e = threadIdx.x; e <= E; e += 256) {
+    if (e < E) counts[e] = 0;
+    offsets[e] = 0;
+  }
+}
+
+// Absent routes have row -1; no row past the buffer is touched either.
+__device__ __forceinline__ bool row_here(int64_t row, int64_t R) { return (uint64_t)row < (uint64_t)R; }
+
+// A row kernel's workgroup: `th` threads (whole waves) per token, several
+// tokens where one wave is enough.
+struct RowShape {
+  dim3 grid, block;
+};
+RowShape row_shape(int64_t T, int d) {
+  int th = (int)ceil_div(ceil_div(d, kSlot * 2), 64) * 64;  // two slots per thread
+  th = th > 1024 ? 1024 : th;
+  const int tok = th >= 256 ? 1 : 256 / th;
+  return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
+                                                         const int32_t* __restrict__ token_row, void* __restrict__ xp,
+                                                         int64_t T, int k, int d) {
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) return;
+  for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
+    const Slot<F32> s = load_slot<F32>(x, t * d + c, d - c);
+    for (int j = 0; j < k; ++j) {
+      const int64_t row = token_row[t * k + j];
+      if (row_here(row, T * k)) store_slot<F32>(xp, row * d + c, d - c, s);
+    }
+  }
+}
+
+// y[t] = sum_j w_j rows[row_j] + add[t]; w NULL: every weight 1, add NULL: 0.
+// add may be y: a slot is read before the thread that read it writes it.
+template <bool F32>
+__global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ rows,
+                                                      const int32_t* __restrict__ token_row,
+                                                      const float* __restrict__ w, const void* add, void* y, int64_t T,
+                                                      int k, int d) {
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) return;
+  for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
+    float acc[kSlot] = {}, v[kSlot];
+    for (int j = 0; j < k; ++j) {
+      const int64_t row = token_row[t * k + j];
+      if (!row_here(row, T * k)) continue;
+      const float g = w ? w[t * k + j] : 1.0f;
+      unpack_slot<F32>(load_slot<F32>(rows, row * d + c, d - c), v);
+#pragma unroll
+      for (int i = 0; i < kSlot; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+    }
+    if (add) {
+      unpack_slot<F32>(load_slot<F32>(add, t * d + c, d - c), v);
+#pragma unroll
+      for (int i = 0; i < kSlot; ++i) acc[i] += v[i];
+    }
+    store_slot<F32>(y, t * d + c, d - c, pack_slot<F32>(acc));
+  }
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ o,
+                                                          const int32_t* __restrict__ token_row,
+                                                          const float* __restrict__ w, void* __restrict__ dov,
+                                                          float* __restrict__ dw, int64_t T, int k, int d) {
+  __shared__ float part[16];
+  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (t >= T) return;  // several tokens only where each is one wave: no barrier below
+  const int waves = blockDim.x / 64;
+  for (int j = 0; j < k; ++j) {
+    const int64_t row = token_row[t * k + j];
+    if (!row_here(row, T * k)) {
+      if (dw && threadIdx.x == 0) dw[t * k + j] = 0.0f;
+      continue;
+    }
+    const float g = dov ? w[t * k + j] : 0.0f;  // the weights may be missing where only dw is wanted
+    float dot = 0.0f, a[kSlot], b[kSlot];
+    for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
+      unpack_slot<F32>(load_slot<F32>(dy, t * d + c, d - c), a);
+      if (dw) {
+        unpack_slot<F32>(load_slot<F32>(o, row * d + c, d - c), b);
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) dot = fmaf(a[i], b[i], dot);
+      }
+      if (dov) {
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) b[i] = g * a[i];
+        store_slot<F32>(dov, row * d + c, d - c, pack_slot<F32>(b));
+      }
+    }
+    if (!dw) continue;
+    dot = wave_sum(dot);
+    if (waves > 1) {
+      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      dot = 0.0f;
+      for (int i = 0; i < waves; ++i) dot += part[i];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) dw[t * k + j] = dot;
+  }
+}
+
+}  // namespace
+
+size_t sort_scratch_bytes(int64_t T, int k, int E) {
+  return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
+}
+
+hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k,
+                       int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm,
+                       void* scratch, hipStream_t s) {
+  if (T == 0) {
+    sort_empty_kernel<<<1, 256, 0, s>>>(counts, offsets, E);
+    return hipGetLastError();
+  }
+  const int64_t R = T * k;
+  const unsigned nb = (unsigned)ceil_div(R, kSortRoutes);
+  int32_t* bc = static_cast<int32_t*>(scratch);
+  sort_count_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, bc);
+  sort_scan_kernel<<<(unsigned)E, 256, 0, s>>>(bc, (int)nb, counts);
+  sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
+  if (x_perm) {
+    const RowShape g = row_shape(T, d);
+    (f32 ? sort_rows_kernel<true> : sort_rows_kernel<false>)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, const float* w, const void* add, void* y,
+                         int64_t T, int d, int k, hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  const RowShape g = row_shape(T, d);
+  (f32 ? unsort_kernel<true> : unsort_kernel<false>)<<<g.grid, g.block, 0, s>>>(rows, token_row, w, add, y, T, k, d);
+  return hipGetLastError();
+}
+
+hipError_t launch_unsort_bwd(bool f32, const void* dy, const void* o_perm, const int32_t* token_row, const float* w,
+                             void* do_perm, float* dw, int64_t T, int d, int k, hipStream_t s) {
+  if (T == 0) return hipSuccess;
+  const RowShape g = row_shape(T, d);
+  (f32 ? unsort_bwd_kernel<true> : unsort_bwd_kernel<false>)<<<g.grid, g.block, 0, s>>>(dy, o_perm, token_row, w,
+                                                                                        do_perm, dw, T, k, d);
+  return hipGetLastError();
+}
+
+}  // namespace moe

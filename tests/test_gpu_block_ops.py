@@ -1,0 +1,408 @@
+"""The operators around the layer on the GPU, each against its definition in
+64 bits (tests/block_ref.py holds the references and the error bounds), with
+absent routes, odd sizes, rows at any element, untouched tails, streams,
+captured graphs and repeated calls."""
+import pytest
+
+import mixture_experts_layer_prefix_amd as M
+
+torch = pytest.importorskip("torch")
+from tests import block_ref as B  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(g, shape, dtype=torch.float32, scale=1.0, odd=False):
+    """Normal values; odd: at an address that is a multiple of the element
+    size only."""
+    n = 1
+    for s in shape:
+        n *= s
+    t = (torch.randn(n + 1, generator=g, device="cuda") * scale).to(dtype)
+    return (t[1:] if odd else t[:-1]).view(shape)
+
+
+def routes(g, T, E, k, absent):
+    idx = torch.randint(0, E, (T, k), generator=g, device="cuda", dtype=torch.int32)  # ids may repeat in a token
+    if absent == "some":
+        u = torch.rand(T, k, generator=g, device="cuda")
+        idx = torch.where(u < 0.2, -1, torch.where(u > 0.9, E + 3, idx))
+        idx[torch.rand(T, generator=g, device="cuda") < 0.2] = -1
+    elif absent == "all":
+        idx = torch.full_like(idx, -7)
+    return idx.to(torch.int32).contiguous()
+
+
+# ---- sort ------------------------------------------------------------------
+@pytest.mark.parametrize("prec", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,k,absent", [
+    (1, 7, 1, 1, "none"), (1, 64, 256, 8, "some"), (5, 33, 3, 4, "some"), (16, 1000, 64, 8, "none"),
+    (33, 8, 1024, 16, "some"), (700, 130, 5, 3, "some"), (2500, 24, 300, 6, "none"), (9000, 16, 17, 8, "some"),
+    (257, 72, 8, 2, "all"), (40, 9001, 32, 2, "some")])
+def test_sort(T, d, E, k, absent, prec):
+    g = gen(T + d)
+    dims = M.Dims(T, d, E, k, 1)
+    idx, x = routes(g, T, E, k, absent), randn(g, (T, d), TYPES[prec], odd=True)
+    x_perm = torch.full((T * k, d), 7.0, dtype=TYPES[prec], device="cuda")
+    row_token = torch.full((T * k,), -5, dtype=torch.int32, device="cuda")
+    plan = M.SortPlan(dims, prec, x_perm=x_perm, row_token=row_token)
+    for _ in range(2):
+        counts, offsets, row_token, token_row, x_perm = plan.run(idx, x)
+        c, o, rt, tr = B.sort_ref(idx.cpu(), E)
+        n = int(o[-1])
+        assert torch.equal(counts.cpu(), c) and torch.equal(offsets.cpu(), o) and torch.equal(token_row.cpu(), tr)
+        assert torch.equal(row_token[:n].cpu(), rt) and bool((row_token[n:] == -5).all())
+        assert torch.equal(x_perm[:n], x[rt.long().cuda()]) and bool((x_perm[n:] == 7.0).all())
+        x_perm.fill_(7.0)
+    sched = M.sort_tokens(idx, None, dims, prec, gather=False)
+    assert sched[4] is None and torch.equal(sched[3], token_row) and torch.equal(sched[2][:n], row_token[:n])
+
+
+def test_sort_equals_permute_where_every_route_is_present():
+    g = gen(3)
+    T, d, E, k = 1500, 128, 48, 6
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.sort(1).values.to(torch.int32)
+    x = randn(g, (T, d), torch.bfloat16)
+    dims = M.Dims(T, d, E, k, 64)
+    for a, b in zip(M.sort_tokens(idx, x, dims, "bf16"), M.permute(idx, x, dims, "bf16")[:5]):
+        assert torch.equal(a, b)
+
+
+def test_empty_batch():
+    dims = M.Dims(0, 24, 6, 2, 1)
+    e = torch.empty
+    counts, offsets, _, _, _ = M.sort_tokens(e(0, 2, dtype=torch.int32, device="cuda"), e(0, 24, device="cuda"), dims,
+                                             "f32")
+    assert counts.tolist() == [0] * 6 and offsets.tolist() == [0] * 7
+    tr = e(0, 2, dtype=torch.int32, device="cuda")
+    assert M.unsort_tokens(e(0, 24, device="cuda"), tr, e(0, 2, device="cuda"), None, dims, "f32").shape == (0, 24)
+    b = M.Block(0, 24, "f32", post_norm=True)
+    z = e(0, 24, device="cuda")
+    w = torch.ones(24, device="cuda")
+    x_out, a, plan = M.block_norm(b, z, z, w, w)
+    assert x_out.shape == a.shape == (0, 24)
+    _, _, grads = M.block_norm_backward(b, z, z, z, z, plan.r_pre, plan.r_post, w, w)
+    assert not grads["dw_pre"].any() and not grads["dw_post"].any()
+
+
+# ---- unsort and the gradients ----------------------------------------------
+UNSORT = [(1, 7, 1, "none"), (1, 200, 8, "some"), (5, 33, 4, "some"), (16, 1024, 8, "none"), (33, 8, 16, "some"),
+          (70, 130, 3, "some"), (64, 513, 12, "some"), (20, 4100, 6, "none"), (257, 72, 2, "all"), (12, 9001, 5, "some")]
+
+
+def unsort_inputs(T, d, k, absent, prec, seed):
+    """Rows and weights that no present route reads hold NaN."""
+    g = gen(seed)
+    E = 11
+    idx = routes(g, T, E, k, absent)
+    _, offsets, _, token_row = B.sort_ref(idx.cpu(), E)
+    token_row = token_row.cuda()
+    rows = randn(g, (T * k, d), TYPES[prec], odd=True)
+    rows[int(offsets[-1]):] = float("nan")
+    w = torch.rand(T, k, generator=g, device="cuda")
+    w[token_row < 0] = float("nan")
+    return M.Dims(T, d, E, k, 1), rows, token_row, w, randn(g, (T, d), TYPES[prec]), int(offsets[-1])
+
+
+@pytest.mark.parametrize("prec", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,k,absent", UNSORT)
+def test_unsort_and_sort_backward(T, d, k, absent, prec):
+    dims, rows, token_row, w, add, _ = unsort_inputs(T, d, k, absent, prec, T * 3 + d)
+    for a in (None, add):
+        ref, mag = B.unsort_ref(rows, token_row.cpu(), w.cpu(), a)
+        y = M.unsort_tokens(rows, token_row, w, a, dims, prec)
+        B.check("y", y, ref, mag, k + 1)  # k fma and the addend
+        ref, mag = B.unsort_ref(rows, token_row.cpu(), None, a)
+        dx = M.sort_tokens_backward(rows, token_row, a, dims, prec)
+        B.check("dx", dx, ref, mag, k + 1)
+    into = add.clone()
+    assert M.sort_tokens_backward(rows, token_row, into, dims, prec, dx=into) is into and torch.equal(into, dx)
+
+
+def test_unsort_equals_combine_where_every_route_is_present():
+    g = gen(4)
+    T, d, E, k = 300, 256, 20, 5
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.sort(1).values.to(torch.int32)
+    dims = M.Dims(T, d, E, k, 64)
+    token_row = M.sort_tokens(idx, None, dims, "bf16", gather=False)[3]
+    o, w, ys = randn(g, (T * k, d), torch.bfloat16), torch.rand(T, k, generator=g, device="cuda"), randn(
+        g, (T, d), torch.bfloat16)
+    assert torch.equal(M.unsort_tokens(o, token_row, w, ys, dims, "bf16"), M.combine(o, token_row, w, ys, dims, "bf16"))
+
+
+@pytest.mark.parametrize("prec", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,k,absent", UNSORT)
+def test_unsort_backward(T, d, k, absent, prec):
+    dims, rows, token_row, w, dy, n = unsort_inputs(T, d, k, absent, prec, T * 5 + d)
+    do_perm = torch.full((T * k, d), 9.0, dtype=TYPES[prec], device="cuda")
+    do, dw = M.unsort_tokens_backward(dy, rows, token_row, w, dims, prec, do_perm=do_perm)
+    rdo, rdw, mag = B.unsort_bwd_ref(dy, rows, token_row.cpu(), w.cpu())
+    # a thread's share of a row of d <= 16384 is at most 16 products, as in ROW_SUM
+    B.check("dtopk_w", dw, rdw, mag, B.ROW_SUM + 1)
+    assert bool((dw[token_row < 0] == 0).all())
+    for row, ref in rdo.items():
+        B.check("do_perm", do[row], ref, ref.abs(), 1)
+    assert bool((do[n:] == 9.0).all())
+    # either output alone, the same bits
+    only, none = M.unsort_tokens_backward(dy, None, token_row, w, dims, prec, need_dw=False)
+    assert none is None and torch.equal(only[:n], do[:n])
+    none, only = M.unsort_tokens_backward(dy, rows, token_row, None, dims, prec, need_do=False)
+    assert none is None and torch.equal(only, dw)
+
+
+# ---- block norm ------------------------------------------------------------
+NORMS = [  # T, d, gate_every (0: no gate, -1: one gate row), post, alpha, beta
+    (1, 7168, 0, False, 1.0, 1.0), (1, 1, -1, True, 0.5, 2.0), (3, 64, 1, True, 1.0, 1.0), (5, 33, 2, True, -0.75, 0.5),
+    (64, 512, -1, False, 0.875, 1.0), (70, 513, 7, True, 1.0, 0.25), (33, 2047, 100, True, 0.5, 1.5),
+    (130, 1000, 33, False, 1.0, 1.0), (9, 8193, 4, True, 1.0, 0.5), (4, 16384, -1, True, 0.5, 1.0),
+    (1100, 40, 500, True, 0.75, 0.5), (1537, 72, -1, True, 1.0, 1.0), (1030, 16, 1, True, 1.0, 1.0),
+    (1600, 24, 5, False, 1.0, 1.0)]
+PRECS = [("bf16", False), ("bf16", True), ("f32", False)]
+
+
+def norm_inputs(T, d, every, post, alpha, beta, prec, res_f32, seed, odd=False):
+    g = gen(seed)
+    block = M.Block(T, d, prec, res_f32=res_f32, post_norm=post, alpha=alpha, beta=beta, eps=1e-5,
+                    gate_every=max(every, 0))
+    p = dict(x=randn(g, (T, d), block.res, 2.0, odd), y=randn(g, (T, d), block.act, 0.7, odd),
+             w_pre=randn(g, (d,), odd=odd), w_post=randn(g, (d,), odd=odd) if post else None,
+             gate=randn(g, (block.gates, d), odd=odd) if every else None)
+    p["y"][T // 2] = 0.0  # a row without a norm
+    return block, p
+
+
+@pytest.mark.parametrize("prec,res_f32", PRECS)
+@pytest.mark.parametrize("T,d,every,post,alpha,beta", NORMS)
+def test_block_norm(T, d, every, post, alpha, beta, prec, res_f32):
+    block, p = norm_inputs(T, d, every, post, alpha, beta, prec, res_f32, T + d, odd=d % 2 == 1)
+    args = (p["x"], p["y"], p["w_post"], p["gate"], p["w_pre"], block.every, alpha, beta, 1e-5, post)
+    ref, mag = B.norm_fwd_ref(*args), B.norm_fwd_ref(*args, magnitude=True)
+    x_out, a, plan = M.block_norm(block, p["x"], p["y"], p["w_pre"], p["w_post"], p["gate"])
+    # eps is rounded to fp32 (it counts as one rounding); r: half the sum's error, mean, root, quotient
+    stat = B.ROW_SUM // 2 + 5
+    if post:
+        B.check("r_post", plan.r_post, ref["r_post"], ref["r_post"], stat)
+    B.check("x_out", x_out, ref["x_out"], mag["x_out"], stat + 5)
+    B.check("r_pre", plan.r_pre, ref["r_pre"], mag["r_pre"], 2 * stat + 5)
+    B.check("a", a, ref["a"], mag["a"], 2 * stat + 8)
+    # the two halves alone: x' without the next norm, the norm without a block output
+    alone, none, _ = M.block_norm(block, p["x"], p["y"], None, p["w_post"], p["gate"], pre_norm=False)
+    assert none is None and torch.equal(alone, x_out)
+    pre = M.Block(T, d, prec, res_f32=res_f32, eps=1e-5)
+    same, a2, plan2 = M.block_norm(pre, p["x"], w_pre=p["w_pre"])
+    assert same is p["x"]
+    args = (p["x"], None, None, None, p["w_pre"], 1, 1.0, 1.0, 1e-5, False)
+    ref, mag = B.norm_fwd_ref(*args), B.norm_fwd_ref(*args, magnitude=True)
+    B.check("r_pre", plan2.r_pre, ref["r_pre"], ref["r_pre"], stat)
+    B.check("a", a2, ref["a"], mag["a"], stat + 2)
+
+
+@pytest.mark.parametrize("prec,res_f32", PRECS)
+@pytest.mark.parametrize("T,d,every,post,alpha,beta", NORMS)
+def test_block_norm_backward(T, d, every, post, alpha, beta, prec, res_f32):
+    block, p = norm_inputs(T, d, every, post, alpha, beta, prec, res_f32, T + 2 * d, odd=d % 2 == 1)
+    g = gen(7)
+    x_out, _, plan = M.block_norm(block, p["x"], p["y"], p["w_pre"], p["w_post"], p["gate"])
+    dxo, da = randn(g, (T, d), block.res, 0.3), randn(g, (T, d), block.act, 0.2)
+
+    def both(dxo, da, x_out, y, w_post, gate, w_pre, blk, r_pre, r_post):
+        got = M.block_norm_backward(blk, dxo, da, x_out, y, r_pre, r_post, w_pre, w_post, gate)
+        args = (dxo, da, x_out, y, r_post, r_pre, w_post, gate, w_pre, blk.every, blk.alpha, blk.beta, blk.post_norm)
+        return got, B.norm_bwd_ref(*args), B.norm_bwd_ref(*args, magnitude=True)
+
+    # roundings: two row sums and a dozen products; a sum over tokens adds at
+    # most 3 + 16 + 32 + 16 more (the tokens of a team, the teams: T <= 1600)
+    row, col = 2 * B.ROW_SUM + 16, 2 * B.ROW_SUM + 16 + 67
+    (dx, dy, grads), ref, mag = both(dxo, da, x_out, p["y"], p["w_post"], p["gate"], p["w_pre"], block, plan.r_pre,
+                                     plan.r_post)
+    B.check("dx", dx, ref["dx"], mag["dx"], row)
+    B.check("dy", dy, ref["dy"], mag["dy"], row)
+    assert set(grads) == {n for n in ("dw_pre", "dw_post", "dgate") if n in ref}
+    for n, t in grads.items():
+        B.check(n, t, ref[n], mag[n], col)
+    # the step after the last block (no da), and the one before the first (no y)
+    (dx, dy, grads), ref, mag = both(dxo, None, None, p["y"], p["w_post"], p["gate"], None, block, None, plan.r_post)
+    B.check("dx", dx, ref["dx"], mag["dx"], row)
+    B.check("dy", dy, ref["dy"], mag["dy"], row)
+    assert "dw_pre" not in grads
+    for n, t in grads.items():
+        B.check(n, t, ref[n], mag[n], col)
+    pre = M.Block(T, d, prec, res_f32=res_f32, eps=1e-5)
+    _, _, plan = M.block_norm(pre, p["x"], w_pre=p["w_pre"])
+    for d0 in (dxo, None):
+        (dx, dy, grads), ref, mag = both(d0, da, p["x"], None, None, None, p["w_pre"], pre, plan.r_pre, None)
+        assert dy is None and set(grads) == {"dw_pre"}
+        B.check("dx", dx, ref["dx"], mag["dx"], row)
+        B.check("dw_pre", grads["dw_pre"], ref["dw_pre"], mag["dw_pre"], col)
+
+
+def test_block_norm_in_place_residual():
+    block, p = norm_inputs(37, 300, -1, True, 0.5, 1.5, "bf16", False, 1)
+    x_out, a, _ = M.block_norm(block, p["x"], p["y"], p["w_pre"], p["w_post"], p["gate"])
+    plan = M.BlockNormPlan(block)
+    plan.x_out = p["x"]
+    got, b = plan.run(p["x"], p["y"], p["w_pre"], p["w_post"], p["gate"])
+    assert got is p["x"] and torch.equal(got, x_out) and torch.equal(a, b)
+
+
+def test_wrappers_refuse_wrong_tensors():
+    block, p = norm_inputs(8, 64, -1, True, 1.0, 1.0, "bf16", False, 1)
+    for bad in (dict(x=p["x"].float()), dict(x=p["x"][:4]), dict(y=p["y"].t().contiguous().t()),
+                dict(y=p["y"].cpu()), dict(w_pre=p["w_pre"].bfloat16()), dict(gate=torch.ones(2, 64, device="cuda"))):
+        with pytest.raises(ValueError):
+            M.block_norm(block, **{**p, **bad})
+    dims = M.Dims(8, 64, 4, 2, 1)
+    idx = torch.zeros(8, 2, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        M.sort_tokens(idx, p["x"], dims, "bf16")
+    with pytest.raises(ValueError):
+        M.sort_tokens(idx.int(), None, dims, "bf16")
+    with pytest.raises(ValueError):
+        M.clip_grads([p["x"], p["x"]], 1.0)
+    with pytest.raises(ValueError):
+        M.clip_grads([p["x"]], 1.0, out=[p["x"].float()])
+    with pytest.raises(ValueError):
+        M.clip_grads([p["x"].half()], 1.0)
+    with pytest.raises(ValueError):
+        M.clip_grads([p["x"]], 1.0, norm=torch.ones(2, device="cuda"))
+
+
+# ---- gradient norm and clipping --------------------------------------------
+CLIPS = [[(5,)], [(1,), (3, 3), (0,), (129,)], [(16384,), (16385,), (40000,), (7, 11)], [(64, 64)] * 9,
+         [(i % 37,) for i in range(700)], [(2100000,), (31,)], [(0,), (0, 4)]]
+
+
+@pytest.mark.parametrize("types", ["bf16", "f32", "mixed"])
+@pytest.mark.parametrize("shapes", CLIPS, ids=range(len(CLIPS)))
+def test_clip(shapes, types):
+    g = gen(len(shapes))
+    grads = [randn(g, s, torch.float32 if types == "f32" or (types == "mixed" and i % 3 == 1) else torch.bfloat16,
+                   10.0 ** (i % 5 - 2), odd=i % 2 == 1) for i, s in enumerate(shapes)]
+    ref = torch.stack([B.f64(t).pow(2).sum() for t in grads]).sum().sqrt()
+    norm = M.grad_norm(grads)
+    # 64-bit sums (2^22 terms leave 2^-31), one rounding to fp32
+    assert abs(norm.double().cpu() - ref) <= ref * (B.U + 2.0 ** -31)
+    exact = float(norm)
+    for max_norm in (0.37 * exact, exact + 1.0, 0.0):
+        f = min(1.0, max_norm / (exact + 1e-6))
+        out, n2 = M.clip_grads(grads, max_norm, out=[torch.empty_like(t) for t in grads])
+        assert torch.equal(n2, norm)
+        for o, t in zip(out, grads):
+            B.check("clipped", o, B.f64(t) * f, (B.f64(t) * f).abs(), 3)  # max_norm to fp32, sum, quotient
+            assert f < 1.0 or torch.equal(o, t)
+        given, n3 = M.clip_grads(grads, max_norm, norm=norm, out=[torch.empty_like(t) for t in grads])
+        assert n3 is norm and all(torch.equal(a, b) for a, b in zip(given, out))
+    out, _ = M.clip_grads(grads, 0.37 * exact, out=[torch.empty_like(t) for t in grads])
+    same, n4 = M.clip_grads(grads, 0.37 * exact)  # in place
+    assert same is grads and torch.equal(n4, norm) and all(torch.equal(a, b) for a, b in zip(grads, out))
+
+
+def test_clip_in_place_leaves_small_gradients():
+    g = gen(8)
+    grads = [randn(g, (1000,), torch.bfloat16), randn(g, (333,))]
+    keep = [t.clone() for t in grads]
+    _, norm = M.clip_grads(grads, 1e6)
+    assert float(norm) > 1.0 and all(torch.equal(a, b) for a, b in zip(grads, keep))
+
+
+def test_norm_of_values_whose_squares_leave_fp32():
+    grads = [torch.full((1000,), 1e25, device="cuda"), torch.full((4,), 1e-30, device="cuda")]
+    assert abs(float(M.grad_norm(grads)) / (1000 ** 0.5 * 1e25) - 1) < 1e-6
+    small = [torch.full((100,), 1e-30, device="cuda")]
+    assert abs(float(M.grad_norm(small)) / 1e-29 - 1) < 1e-6
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_clip_of_gradients_that_are_not_finite(bad):
+    grads = [torch.ones(50, device="cuda"), torch.ones(20000, device="cuda", dtype=torch.bfloat16)]
+    grads[1][17] = bad
+    out, norm = M.clip_grads(grads, 1.0, out=[torch.empty_like(t) for t in grads])
+    if bad != bad:
+        assert bool(norm.isnan()) and all(bool(t.isnan().all()) for t in out)
+    else:
+        assert bool(norm.isinf()) and bool((out[0] == 0).all()) and bool(out[1][17].isnan())
+        assert int((out[1] == 0).sum()) == 19999
+
+
+def test_clip_of_a_tensor_of_more_than_2_30_elements():
+    n = (1 << 30) + 12345
+    t = torch.full((n,), 0.5, dtype=torch.bfloat16, device="cuda")
+    norm = M.grad_norm([t])
+    assert abs(float(norm) / (0.5 * n ** 0.5) - 1) < 1e-6
+    M.clip_grads([t], float(norm) / 4)
+    assert bool((t == 0.125).all())
+
+
+# ---- streams, graphs, repeats ----------------------------------------------
+def step_inputs():
+    T, d, E, k = 600, 200, 12, 4
+    block, p = norm_inputs(T, d, 50, True, 0.75, 0.5, "bf16", True, 2)
+    g = gen(12)
+    idx = routes(g, T, E, k, "some")
+    return T, d, E, k, block, p, idx, torch.rand(T, k, generator=g, device="cuda"), g
+
+
+class Step:
+    """norm, sort, unsort, their gradients and a clip, into buffers of its own."""
+
+    def __init__(self):
+        self.T, self.d, self.E, self.k, self.block, self.p, self.idx, self.w, g = step_inputs()
+        self.dims = M.Dims(self.T, self.d, self.E, self.k, 1)
+        self.norm = M.BlockNormPlan(self.block)
+        self.sort = M.SortPlan(self.dims, "bf16")
+        self.sort.x_perm.zero_()
+        self.sort.row_token.zero_()
+        self.back = M.BlockNormBackwardPlan(self.block, gate=True)
+        self.do = torch.zeros_like(self.sort.x_perm)
+        self.dxo = randn(g, (self.T, self.d), torch.float32)
+
+    def run(self):
+        p = self.p
+        x_out, a = self.norm.run(p["x"], p["y"], p["w_pre"], p["w_post"], p["gate"])
+        token_row, x_perm = self.sort.run(self.idx, a)[3:]
+        y = M.unsort_tokens(x_perm, token_row, self.w, a, self.dims, "bf16")
+        do, dw = M.unsort_tokens_backward(y, x_perm, token_row, self.w, self.dims, "bf16", do_perm=self.do)
+        da = M.sort_tokens_backward(do, token_row, y, self.dims, "bf16")
+        dx, dy, grads = self.back.run(self.dxo, da, x_out, p["y"], self.norm.r_pre, self.norm.r_post, p["w_pre"],
+                                      p["w_post"], p["gate"])
+        some = [dx, dy, dw] + list(grads.values())
+        out, norm = M.clip_grads(some, 1.0, out=[torch.empty_like(t) for t in some])
+        return [x_out, a, y, do, dw, da, dx, dy, norm] + list(grads.values()) + out
+
+
+def test_step_repeats_bit_for_bit_on_any_stream():
+    step = Step()
+    first = [t.clone() for t in step.run()]
+    assert all(torch.equal(a, b) for a, b in zip(first, step.run()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step.run()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_captured_step_replays():
+    step, other = Step(), Step()
+    eager = [t.clone() for t in step.run()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step.run()
+    for i in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(eager, other.run()))  # eager work of its own in between
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(eager, got)), "replay %d" % i
+    step.p["x"].mul_(0.5)  # a replay reads its inputs anew
+    graph.replay()
+    fresh = Step()
+    fresh.p["x"].mul_(0.5)
+    assert all(torch.equal(a, b) for a, b in zip(fresh.run(), got))
