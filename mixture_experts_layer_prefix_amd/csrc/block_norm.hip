@@ -24,24 +24,25 @@ namespace moe {
 
 namespace {
 
-// Sums of NV values over the `waves` waves of a workgroup (blockDim.y == 1)
-// in wave order; each exchange alternates between the halves of `lds`, so
-// that one barrier per exchange is enough.  One wave: no exchange.
+// Sums of NV values over the `waves` waves of a team in wave order, for all
+// teams of the workgroup at once; exchanges alternate between the halves of
+// `lds`, so that one barrier each is enough.  One wave: no exchange.
 template <int NV>
 __device__ __forceinline__ void team_sum(float (&v)[NV], float (*lds)[16][NV], int waves, int& phase) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
   if (waves == 1) return;
+  const int first = threadIdx.y * waves;
   if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) lds[phase][threadIdx.x >> 6][i] = v[i];
+    for (int i = 0; i < NV; ++i) lds[phase][first + (threadIdx.x >> 6)][i] = v[i];
   }
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NV; ++i) v[i] = 0.0f;
   for (int w = 0; w < waves; ++w) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += lds[phase][w][i];
+    for (int i = 0; i < NV; ++i) v[i] += lds[phase][first + w][i];
   }
   phase ^= 1;
 }
@@ -122,171 +123,253 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(BlockNorm p) {
   }
 }
 
-// Team b owns the rows [b * per, (b + 1) * per).  The gradients of the
-// weights are summed over the team's rows in registers and left as row b of
-// part_pre and part_post.  dgate of a group inside the team's rows is whole;
-// a group that began in an earlier team goes to row 2b of part_gate, one that
-// began here and goes on to row 2b + 1.  sum_parts_kernel adds the rows.
+// The raw slots of one row: x', da, dx', y.
 template <bool AF32, bool RF32, int VPT>
+struct BwdRow {
+  Slot<RF32> x[VPT], d[VPT];
+  Slot<AF32> a[VPT], y[VPT];
+};
+
+// Workgroups of up to 16 waves, one per compute unit; a workgroup holds
+// blockDim.y teams of blockDim.x threads, team b the rows [b per, (b+1) per),
+// one at a time.  All teams of a workgroup take the same number of steps, so
+// that one barrier serves them.  Each thread owns VPT slots of columns: w_pre
+// and c = beta gate w_post stay in its registers, as do the column sums
+//   sum_t da xh  and  A = sum_t dz yh,
+// from which dgate_g = beta w_post A and dw_post = sum_g beta gate_g A_g.
+// Where all tokens share a gate row (or there is none) A is one more column
+// sum; with several gate rows, a group inside the team's rows is written
+// whole, a group that began in an earlier team goes to row 2b of part_gate
+// and one that begins here and goes on to row 2b + 1.  The teams' column sums
+// are added over the workgroup and left as its row of part_pre and part_post
+// (A where there is one gate row); sum_parts_kernel adds those rows.
+// The next row's loads are in flight while a row is worked on (PREFETCH).
+// MANY: several gate rows.  TAIL: d is not a multiple of the slot.
+template <bool AF32, bool RF32, int VPT, bool PREFETCH, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
-  __shared__ float lds[2][16][3];
+  __shared__ float red[2][16][3];
+  __shared__ float cols[1024 * kSlot];
   const int64_t b = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   const int64_t t0 = b * p.per, t1 = min(t0 + p.per, p.T);
-  if (t0 >= p.T) return;  // several teams only where each is one wave: no barrier below
   const int waves = blockDim.x / 64, d = p.d;
   int phase = 0;
-  float acc_pre[VPT][kSlot] = {}, acc_post[VPT][kSlot] = {}, acc_gate[VPT][kSlot] = {};
-  for (int64_t t = t0; t < t1; ++t) {
-    const int64_t g = p.gate ? t / p.gate_every : 0;
-    const float r2 = p.da ? p.r_pre[t] : 0.0f, r1 = p.post_norm ? p.r_post[t] : 1.0f;
-    float sum[3] = {0.0f, 0.0f, 0.0f};
-    Slot<RF32> xs[VPT], ds[VPT];
-    Slot<AF32> ys[VPT], as[VPT];
+  float w_pre[VPT][kSlot], c[VPT][kSlot];
+  float acc_pre[VPT][kSlot] = {}, acc_a[VPT][kSlot] = {}, acc_post[VPT][kSlot] = {};  // acc_post: MANY only
+
+  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
+  auto vec = [&](const float* v, int64_t e, int left, float (&out)[kSlot]) {
+    if (v) {
+      unpack_slot<true>(load_slot<true, TAIL>(v, e, left), out);
+    } else {
 #pragma unroll
-    for (int q = 0; q < VPT; ++q) {
-      const int c = (q * blockDim.x + threadIdx.x) * kSlot, left = d - c;
-      const int64_t e = t * d + c;
-      xs[q] = p.da ? load_slot<RF32>(p.x_out, e, left) : Slot<RF32>{};
-      as[q] = p.da ? load_slot<AF32>(p.da, e, left) : Slot<AF32>{};
-      ds[q] = p.dx_out ? load_slot<RF32>(p.dx_out, e, left) : Slot<RF32>{};
-      ys[q] = p.y ? load_slot<AF32>(p.y, e, left) : Slot<AF32>{};
+      for (int i = 0; i < kSlot; ++i) out[i] = 1.0f;
     }
+  };
+  auto load_c = [&](int64_t g) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      const int c = (q * blockDim.x + threadIdx.x) * kSlot, left = d - c;
-      float x[kSlot], a[kSlot], dz[kSlot], y[kSlot], w[kSlot], cf[kSlot];
-      unpack_slot<RF32>(xs[q], x);
-      unpack_slot<AF32>(as[q], a);
-      unpack_slot<RF32>(ds[q], dz);
-      unpack_slot<AF32>(ys[q], y);
-      if (p.w_pre) unpack_slot<true>(load_slot<true>(p.w_pre, c, left), w);
+      float gt[kSlot];
+      vec(p.w_post, column(q), d - column(q), c[q]);
+      vec(p.gate, g * d + column(q), d - column(q), gt);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) {
-        const float xh = x[i] * r2;
-        acc_pre[q][i] = fmaf(a[i], xh, acc_pre[q][i]);
-        const float u = p.w_pre ? a[i] * w[i] : a[i];
-        sum[0] = fmaf(u, xh, sum[0]);
-        dz[i] = fmaf(r2, u, dz[i]);
-        x[i] = xh;
-      }
-      if (p.post_norm) {
-        if (p.w_post) unpack_slot<true>(load_slot<true>(p.w_post, c, left), cf);
-        if (p.gate) unpack_slot<true>(load_slot<true>(p.gate, g * d + c, left), w);
+      for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * gt[i];
+    }
+  };
+  typedef BwdRow<AF32, RF32, VPT> Row;
+  auto load_row = [&](int64_t t, Row& r) {
+#pragma unroll
+    for (int q = 0; q < VPT; ++q) {
+      const int left = d - column(q);
+      const int64_t e = t * d + column(q);
+      r.x[q] = p.da ? load_slot<RF32, TAIL>(p.x_out, e, left) : Slot<RF32>{};
+      r.a[q] = p.da ? load_slot<AF32, TAIL>(p.da, e, left) : Slot<AF32>{};
+      r.d[q] = p.dx_out ? load_slot<RF32, TAIL>(p.dx_out, e, left) : Slot<RF32>{};
+      r.y[q] = p.y ? load_slot<AF32, TAIL>(p.y, e, left) : Slot<AF32>{};
+    }
+  };
+  // One row (t < t1: an idle team only joins the exchange).
+  auto step = [&](int64_t t, const Row& r) {
+    const bool on = t < t1;
+    float r2 = 0.0f, r1 = 1.0f;
+    if (on) {
+      if (p.da) r2 = p.r_pre[t];
+      if (p.post_norm) r1 = p.r_post[t];
+    }
+    float sum[3] = {0.0f, 0.0f, 0.0f};
+    float xh[VPT][kSlot], dz[VPT][kSlot], yh[VPT][kSlot];
+    if (on) {
+#pragma unroll
+      for (int q = 0; q < VPT; ++q) {
+        float a[kSlot];
+        unpack_slot<RF32>(r.x[q], xh[q]);
+        unpack_slot<AF32>(r.a[q], a);
+        unpack_slot<RF32>(r.d[q], dz[q]);
+        unpack_slot<AF32>(r.y[q], yh[q]);
 #pragma unroll
         for (int i = 0; i < kSlot; ++i) {
-          float s = p.beta * (y[i] * r1);
-          if (p.w_post) s *= cf[i];
-          if (p.gate) s *= w[i];
-          sum[1] = fmaf(s, dz[i], sum[1]);
-          sum[2] = fmaf(s * r2, x[i], sum[2]);
+          xh[q][i] *= r2;
+          yh[q][i] *= r1;
+          acc_pre[q][i] = fmaf(a[i], xh[q][i], acc_pre[q][i]);
+          const float u = a[i] * w_pre[q][i];
+          sum[0] = fmaf(u, xh[q][i], sum[0]);
+          dz[q][i] = fmaf(r2, u, dz[q][i]);
+          const float s = c[q][i] * yh[q][i];
+          sum[1] = fmaf(s, dz[q][i], sum[1]);
+          sum[2] = fmaf(s, xh[q][i], sum[2]);
         }
       }
     }
-    team_sum<3>(sum, lds, waves, phase);
-    const float m2 = sum[0] / d, m1 = (sum[1] - m2 * sum[2]) / d;
+    team_sum<3>(sum, red, waves, phase);
+    if (!on) return;
+    const float m2 = r2 * (sum[0] / d), m1 = p.post_norm ? (sum[1] - m2 * sum[2]) / d : 0.0f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      const int c = (q * blockDim.x + threadIdx.x) * kSlot, left = d - c;
-      const int64_t e = t * d + c;
-      float x[kSlot], a[kSlot], dz[kSlot], y[kSlot], w[kSlot], gt[kSlot];
-      unpack_slot<RF32>(xs[q], x);
-      unpack_slot<AF32>(as[q], a);
-      unpack_slot<RF32>(ds[q], dz);
-      if (p.w_pre) unpack_slot<true>(load_slot<true>(p.w_pre, c, left), w);
+      const int left = d - column(q);
+      const int64_t e = t * d + column(q);
+      float out[kSlot];
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
-        const float u = p.w_pre ? a[i] * w[i] : a[i];
-        dz[i] = fmaf(r2, u - (x[i] * r2) * m2, dz[i]);
-        x[i] = p.y ? p.alpha * dz[i] : dz[i];
+        dz[q][i] = fmaf(-m2, xh[q][i], dz[q][i]);
+        out[i] = p.y ? p.alpha * dz[q][i] : dz[q][i];
       }
-      store_slot<RF32>(p.dx, e, left, pack_slot<RF32>(x));
+      store_slot<RF32, TAIL>(p.dx, e, left, pack_slot<RF32>(out));
       if (!p.y) continue;
-      unpack_slot<AF32>(ys[q], y);
-      if (p.w_post) unpack_slot<true>(load_slot<true>(p.w_post, c, left), w);
-      if (p.gate) unpack_slot<true>(load_slot<true>(p.gate, g * d + c, left), gt);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
-        const float ev = p.beta * dz[i], yh = y[i] * r1, wp = p.w_post ? w[i] : 1.0f;
-        acc_gate[q][i] = fmaf(ev, yh * wp, acc_gate[q][i]);
-        const float dn = p.gate ? ev * gt[i] : ev;
-        acc_post[q][i] = fmaf(dn, yh, acc_post[q][i]);
-        y[i] = p.post_norm ? r1 * (dn * wp - yh * m1) : dn;
+        acc_a[q][i] = fmaf(dz[q][i], yh[q][i], acc_a[q][i]);
+        out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
       }
-      store_slot<AF32>(p.dy, e, left, pack_slot<AF32>(y));
+      store_slot<AF32, TAIL>(p.dy, e, left, pack_slot<AF32>(out));
     }
-    // the gate's group ends here, or this team's rows do
-    if (p.dgate && (t + 1 == t1 || (t + 1) % p.gate_every == 0)) {
-      const bool head = g * p.gate_every < t0, tail = t + 1 < p.T && (t + 1) % p.gate_every != 0;
-      float* out = head ? p.part_gate + 2 * b * p.ldp : tail ? p.part_gate + (2 * b + 1) * p.ldp : p.dgate + g * d;
+    if constexpr (!MANY) return;
+    const bool ends = (t + 1) % p.gate_every == 0 || t + 1 == p.T;
+    if (!ends && t + 1 != t1) return;
+    // the gate's group or the team's rows end here: hand A on
+    const int64_t g = t / p.gate_every;
+    float* out = g * p.gate_every < t0 ? p.part_gate + 2 * b * p.ldp
+                 : !ends               ? p.part_gate + (2 * b + 1) * p.ldp
+                                       : p.dgate + g * d;
 #pragma unroll
-      for (int q = 0; q < VPT; ++q) {
-        const int c = (q * blockDim.x + threadIdx.x) * kSlot;
-        store_slot<true>(out, c, d - c, pack_slot<true>(acc_gate[q]));
+    for (int q = 0; q < VPT; ++q) {
+      float wp[kSlot], gt[kSlot];
+      vec(p.w_post, column(q), d - column(q), wp);
+      vec(p.gate, g * d + column(q), d - column(q), gt);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) acc_gate[q][i] = 0.0f;
+      for (int i = 0; i < kSlot; ++i) {
+        const float A = p.beta * acc_a[q][i];
+        wp[i] *= A;
+        acc_post[q][i] = fmaf(gt[i], A, acc_post[q][i]);
+        acc_a[q][i] = 0.0f;
       }
+      if (p.dgate) store_slot<true, TAIL>(out, column(q), d - column(q), pack_slot<true>(wp));
+    }
+    if (ends && t + 1 < t1) load_c(g + 1);
+  };
+
+#pragma unroll
+  for (int q = 0; q < VPT; ++q) vec(p.w_pre, column(q), d - column(q), w_pre[q]);
+  if (t0 < p.T) load_c(MANY ? t0 / p.gate_every : 0);
+  const int64_t end = t0 + p.per;
+  if constexpr (PREFETCH) {
+    Row r0, r1;
+    if (t0 < t1) load_row(t0, r0);
+    for (int64_t t = t0; t < end; t += 2) {
+      if (t + 1 < t1) load_row(t + 1, r1);
+      step(t, r0);
+      if (t + 1 == end) break;
+      if (t + 2 < t1) load_row(t + 2, r0);
+      step(t + 1, r1);
+    }
+  } else {
+    for (int64_t t = t0; t < end; ++t) {
+      Row r;
+      if (t < t1) load_row(t, r);
+      step(t, r);
     }
   }
+
+  // Column sums over the workgroup's teams, in team order.
+  auto leave = [&](float (&acc)[VPT][kSlot], float* part) {
 #pragma unroll
-  for (int q = 0; q < VPT; ++q) {
-    const int c = (q * blockDim.x + threadIdx.x) * kSlot;
-    if (p.dw_pre) store_slot<true>(p.part_pre + b * p.ldp, c, d - c, pack_slot<true>(acc_pre[q]));
-    if (p.dw_post) store_slot<true>(p.part_post + b * p.ldp, c, d - c, pack_slot<true>(acc_post[q]));
+    for (int q = 0; q < VPT; ++q) {
+      if (blockDim.y > 1) {
+        float* mine = cols + (threadIdx.y * blockDim.x + threadIdx.x) * kSlot;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) mine[i] = acc[q][i];
+        __syncthreads();
+        if (threadIdx.y == 0) {
+          for (int k = 1; k < (int)blockDim.y; ++k) {
+#pragma unroll
+            for (int i = 0; i < kSlot; ++i) acc[q][i] += cols[(k * blockDim.x + threadIdx.x) * kSlot + i];
+          }
+        }
+      }
+      if (threadIdx.y == 0)
+        store_slot<true, TAIL>(part + blockIdx.x * p.ldp, column(q), d - column(q), pack_slot<true>(acc[q]));
+    }
+  };
+  if (p.dw_pre) leave(acc_pre, p.part_pre);
+  if constexpr (MANY) {
+    if (p.dw_post) leave(acc_post, p.part_post);
+  } else if (p.dw_post || p.dgate) {
+    leave(acc_a, p.part_post);
   }
 }
 
-// Sums of the teams' rows, 64 columns per workgroup: blockIdx.y 0 is dw_pre,
-// 1 dw_post, 2 + i the i-th gate group that may span teams.  Sixteen threads
-// share four columns, each summing every sixteenth row; the sixteen sums are
-// then added in order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int64_t teams) {
-  __shared__ float lds[16][64];
+// Sums of partial rows, kSumCols columns per workgroup: blockIdx.y 0 is
+// dw_pre; 1 is dw_post and, with one gate row, dgate; 2 + i is the i-th gate
+// group that may span teams.  Eight threads share four columns each, the
+// other 32 ways of the workgroup take the rows in turn; the 32 sums are then
+// added in order.
+constexpr int kSumCols = 32;
+__global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int64_t teams, int64_t groups) {
+  __shared__ float lds[32][kSumCols];
   const int job = blockIdx.y;
-  const float* src;
-  float* dst;
-  int64_t n, first = 0, ld = p.ldp;
-  if (job < 2) {
-    src = job == 0 ? p.part_pre : p.part_post;
-    dst = job == 0 ? p.dw_pre : p.dw_post;
-    n = teams;
-    if (!dst) return;
-  } else {
-    int64_t g = job - 2;
-    const int64_t groups = ceil_div(p.T, p.gate_every);
-    if (groups > teams) g = min(((int64_t)(job - 1) * p.per - 1), p.T - 1) / p.gate_every;  // team's last group
-    const int64_t b0 = g * p.gate_every / p.per, b1 = (min((g + 1) * p.gate_every, p.T) - 1) / p.per;
-    if (b0 == b1 || (groups > teams && b0 != job - 2)) return;
-    src = p.part_gate;
-    dst = p.dgate + g * p.d;
-    // row 2 b0 + 1, then rows 2b for b in (b0, b1]
-    n = b1 - b0 + 1;
-    first = b0;
-    ld = 0;
+  const bool many = p.gate && p.gate_every < p.T;
+  const float* src = p.part_pre;
+  int64_t n = groups, g = 0, first = 0;
+  if (job == 0 && !p.dw_pre) return;
+  if (job == 1) {
+    src = p.part_post;
+    if (!p.dw_post && (many || !p.dgate)) return;
   }
-  const int col = threadIdx.x & 15, sub = threadIdx.x >> 4;
-  const int c = blockIdx.x * 64 + col * 4;
-  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (job >= 2) {
+    const int64_t gates = ceil_div(p.T, p.gate_every);
+    g = job - 2;
+    if (gates > teams) g = (min((g + 1) * p.per, p.T) - 1) / p.gate_every;  // the team's last group
+    first = g * p.gate_every / p.per;
+    const int64_t last = (min((g + 1) * p.gate_every, p.T) - 1) / p.per;
+    if (first == last || (gates > teams && first != job - 2)) return;
+    src = p.part_gate;
+    n = last - first + 1;  // row 2 first + 1, then rows 2b for the teams b after it
+  }
+  const int col = threadIdx.x & 7, sub = threadIdx.x >> 3;
+  const int c = blockIdx.x * kSumCols + col * 4;
+  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < p.ldp) {
-    for (int64_t i = sub; i < n; i += 16) {
-      const int64_t row = ld ? i : (i == 0 ? 2 * first + 1 : 2 * (first + i));
-      const float4 v = *reinterpret_cast<const float4*>(src + row * p.ldp + c);
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
+#pragma unroll 4
+    for (int64_t i = sub; i < n; i += 32) {
+      const int64_t row = job < 2 ? i : 2 * (first + i) + (i == 0);
+      s += *reinterpret_cast<const f32x4*>(src + row * p.ldp + c);
     }
   }
-  lds[sub][col * 4] = s.x;
-  lds[sub][col * 4 + 1] = s.y;
-  lds[sub][col * 4 + 2] = s.z;
-  lds[sub][col * 4 + 3] = s.w;
+  *reinterpret_cast<f32x4*>(&lds[sub][col * 4]) = s;
   __syncthreads();
-  const int out = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && out < p.d) {
-    float v = 0.0f;
+  const int out = blockIdx.x * kSumCols + threadIdx.x;
+  if (threadIdx.x >= kSumCols || out >= p.d) return;
+  float v = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v += lds[i][threadIdx.x];
-    dst[out] = v;
+  for (int i = 0; i < 32; ++i) v += lds[i][threadIdx.x];
+  if (job == 0) {
+    p.dw_pre[out] = v;
+  } else if (job >= 2) {
+    p.dgate[g * p.d + out] = v;
+  } else if (many) {
+    p.dw_post[out] = v;
+  } else {  // v is the column's A
+    if (p.dw_post) p.dw_post[out] = v * (p.gate ? p.beta * p.gate[out] : p.beta);
+    if (p.dgate) p.dgate[out] = v * (p.w_post ? p.beta * p.w_post[out] : p.beta);
   }
 }
 
@@ -303,26 +386,45 @@ void launch_fwd(const BlockNorm& p, hipStream_t s) {
     block_norm_kernel<AF32, RF32, 2><<<grid, block, 0, s>>>(p);
 }
 
-template <bool AF32, bool RF32>
-void launch_bwd(const BlockNormBwd& p, int64_t teams, hipStream_t s) {
-  const int vpt = p.d <= 1024 * kSlot ? 1 : 2, th = team_threads(p.d, vpt), tpb = th == 64 ? 4 : 1;
-  const dim3 grid((unsigned)ceil_div(teams, tpb)), block(th, tpb);
-  if (vpt == 1)
-    block_norm_bwd_kernel<AF32, RF32, 1><<<grid, block, 0, s>>>(p);
-  else
-    block_norm_bwd_kernel<AF32, RF32, 2><<<grid, block, 0, s>>>(p);
+// The backward's workgroups: up to 16 waves, one workgroup per compute unit.
+struct BwdShape {
+  int vpt, th, tpb;      // slots per thread, threads per team, teams per workgroup
+  int64_t per, teams, groups;
+};
+BwdShape bwd_shape(int64_t T, int d) {
+  constexpr int64_t kGroups = 256;
+  BwdShape s;
+  s.vpt = d <= 1024 * kSlot ? 1 : 2;
+  s.th = team_threads(d, s.vpt);
+  s.tpb = 1024 / s.th;
+  s.per = T ? ceil_div(T, kGroups * s.tpb) : 1;
+  s.teams = ceil_div(T, s.per);
+  s.groups = ceil_div(s.teams, s.tpb);
+  return s;
 }
 
-constexpr int64_t kMaxTeams = 512;
-
-// Rows of a team: as even as kMaxTeams teams allow.
-int64_t rows_per_team(int64_t T) { return ceil_div(T, kMaxTeams); }
+template <bool AF32, bool RF32>
+void launch_bwd(const BlockNormBwd& p, const BwdShape& b, hipStream_t s) {
+  auto go = [&](auto kernel) { kernel<<<dim3((unsigned)b.groups), dim3(b.th, b.tpb), 0, s>>>(p); };
+  const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
+  if (b.vpt == 1) {
+    if (many)
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !AF32, true, true>
+              : block_norm_bwd_kernel<AF32, RF32, 1, !AF32, true, false>);
+    else
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, true>
+              : block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, false>);
+  } else {
+    go(many ? block_norm_bwd_kernel<AF32, RF32, 2, false, true, true>
+            : block_norm_bwd_kernel<AF32, RF32, 2, false, false, true>);
+  }
+}
 
 }  // namespace
 
 size_t block_norm_scratch_bytes(int64_t T, int d) {
-  const int64_t teams = T ? ceil_div(T, rows_per_team(T)) : 0;
-  return (size_t)(4 * teams) * (size_t)(ceil_div(d, kSlot) * kSlot) * sizeof(float);
+  const BwdShape b = bwd_shape(T, d);
+  return (size_t)(2 * b.groups + 2 * b.teams) * (size_t)(ceil_div(d, kSlot) * kSlot) * sizeof(float);
 }
 
 hipError_t launch_block_norm(bool act_f32, bool res_f32, const BlockNorm& p, hipStream_t s) {
@@ -337,25 +439,24 @@ hipError_t launch_block_norm(bool act_f32, bool res_f32, const BlockNorm& p, hip
 }
 
 hipError_t launch_block_norm_bwd(bool act_f32, bool res_f32, BlockNormBwd p, void* scratch, hipStream_t s) {
+  const BwdShape b = bwd_shape(p.T, p.d);
   p.ldp = ceil_div(p.d, kSlot) * kSlot;
-  p.per = p.T ? rows_per_team(p.T) : 1;
-  const int64_t teams = ceil_div(p.T, p.per);  // none for an empty batch: the sums below are zero
-  float* part = static_cast<float*>(scratch);
-  p.part_pre = part;
-  p.part_post = part + teams * p.ldp;
-  p.part_gate = part + 2 * teams * p.ldp;
-  if (teams == 0)
-    ;
+  p.per = b.per;
+  p.part_pre = static_cast<float*>(scratch);
+  p.part_post = p.part_pre + b.groups * p.ldp;
+  p.part_gate = p.part_post + b.groups * p.ldp;
+  if (p.T == 0)
+    ;  // no rows: the sums below are zero
   else if (act_f32)
-    launch_bwd<true, true>(p, teams, s);
+    launch_bwd<true, true>(p, b, s);
   else if (res_f32)
-    launch_bwd<false, true>(p, teams, s);
+    launch_bwd<false, true>(p, b, s);
   else
-    launch_bwd<false, false>(p, teams, s);
-  const int64_t groups = p.dgate ? ceil_div(p.T, p.gate_every) : 0;
-  const unsigned jobs = 2 + (unsigned)(groups < teams ? groups : teams);
+    launch_bwd<false, false>(p, b, s);
+  const int64_t gates = p.dgate && p.gate_every < p.T ? ceil_div(p.T, p.gate_every) : 0;
+  const unsigned jobs = 2 + (unsigned)(gates < b.teams ? gates : b.teams);
   if (p.dw_pre || p.dw_post || p.dgate)
-    sum_parts_kernel<<<dim3((unsigned)ceil_div(p.ldp, 64), jobs), 256, 0, s>>>(p, teams);
+    sum_parts_kernel<<<dim3((unsigned)ceil_div(p.ldp, kSumCols), jobs), 256, 0, s>>>(p, b.teams, b.groups);
   return hipGetLastError();
 }
 

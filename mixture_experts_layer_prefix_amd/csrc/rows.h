@@ -26,7 +26,8 @@ struct Slot<true> {
 };
 
 // Elements [0, left) of the slot at element `e` of p; the others read as 0.
-template <bool F32>
+// TAIL false: the row is whole slots, so left is at least 8 or not positive.
+template <bool F32, bool TAIL = true>
 __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int left) {
   Slot<F32> s = {};
   if constexpr (F32) {
@@ -34,7 +35,7 @@ __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int lef
     if (left >= kSlot) {
       s.w = *reinterpret_cast<const u32x4_a4*>(q);
       s.w2 = *reinterpret_cast<const u32x4_a4*>(q + 4);
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < left) s.w[i] = __float_as_uint(q[i]);
@@ -45,7 +46,7 @@ __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int lef
     const bf16_t* q = static_cast<const bf16_t*>(p) + e;
     if (left >= kSlot) {
       s.w = *reinterpret_cast<const u32x4_a2*>(q);
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t v = 0;
@@ -89,14 +90,14 @@ __device__ __forceinline__ Slot<F32> pack_slot(const float (&v)[kSlot]) {
 }
 
 // Writes elements [0, left) of the slot.
-template <bool F32>
+template <bool F32, bool TAIL = true>
 __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const Slot<F32>& s) {
   if constexpr (F32) {
     float* q = static_cast<float*>(p) + e;
     if (left >= kSlot) {
       *reinterpret_cast<u32x4_a4*>(q) = s.w;
       *reinterpret_cast<u32x4_a4*>(q + 4) = s.w2;
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < left) q[i] = __uint_as_float(s.w[i]);
@@ -107,7 +108,7 @@ __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const S
     bf16_t* q = static_cast<bf16_t*>(p) + e;
     if (left >= kSlot) {
       *reinterpret_cast<u32x4_a2*>(q) = s.w;
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (2 * i < left) q[2 * i] = (bf16_t)s.w[i];
