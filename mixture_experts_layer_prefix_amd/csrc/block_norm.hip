@@ -409,8 +409,8 @@ void launch_bwd(const BlockNormBwd& p, const BwdShape& b, hipStream_t s) {
   const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
   if (b.vpt == 1) {
     if (many)
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !AF32, true, true>
-              : block_norm_bwd_kernel<AF32, RF32, 1, !AF32, true, false>);
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !RF32, true, true>
+              : block_norm_bwd_kernel<AF32, RF32, 1, !RF32, true, false>);
     else
       go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, true>
               : block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, false>);

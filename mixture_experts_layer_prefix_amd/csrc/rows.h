@@ -12,6 +12,10 @@ constexpr int kSlot = 8;  // elements per slot: 16 bytes of bf16, 32 of fp32
 
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_a4 __attribute__((aligned(4)));
+typedef uint32_t u32_a2 __attribute__((aligned(2)));
 
 // One slot as loaded: a thread keeps several in flight before it unpacks them.
 template <bool F32>
@@ -27,6 +31,8 @@ struct Slot<true> {
 
 // Elements [0, left) of the slot at element `e` of p; the others read as 0.
 // TAIL false: the row is whole slots, so left is at least 8 or not positive.
+// A partial slot is read and written in pieces of four, two and one elements
+// (one access per bit of left), which the value is shifted together from.
 template <bool F32, bool TAIL = true>
 __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int left) {
   Slot<F32> s = {};
@@ -36,10 +42,17 @@ __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int lef
       s.w = *reinterpret_cast<const u32x4_a4*>(q);
       s.w2 = *reinterpret_cast<const u32x4_a4*>(q + 4);
     } else if constexpr (TAIL) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < left) s.w[i] = __float_as_uint(q[i]);
-        if (i + 4 < left) s.w2[i] = __float_as_uint(q[i + 4]);
+      if (left > 0) {
+        const bool has4 = left & 4, has2 = left & 2;
+        u32x4 four = {};
+        u32x2 two = {};
+        uint32_t one = 0;
+        if (has4) four = *reinterpret_cast<const u32x4_a4*>(q);
+        if (has2) two = *reinterpret_cast<const u32x2_a4*>(q + (left & 4));
+        if (left & 1) one = __float_as_uint(q[left - 1]);
+        const u32x4 rest = has2 ? u32x4{two[0], two[1], one, 0} : u32x4{one, 0, 0, 0};
+        s.w = has4 ? four : rest;
+        s.w2 = has4 ? rest : u32x4{0, 0, 0, 0};
       }
     }
   } else {
@@ -47,12 +60,15 @@ __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int lef
     if (left >= kSlot) {
       s.w = *reinterpret_cast<const u32x4_a2*>(q);
     } else if constexpr (TAIL) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t v = 0;
-        if (2 * i < left) v = q[2 * i];
-        if (2 * i + 1 < left) v |= (uint32_t)q[2 * i + 1] << 16;
-        s.w[i] = v;
+      if (left > 0) {
+        const bool has4 = left & 4, has2 = left & 2;
+        u32x2 four = {};
+        uint32_t two = 0, one = 0;
+        if (has4) four = *reinterpret_cast<const u32x2_a2*>(q);
+        if (has2) two = *reinterpret_cast<const u32_a2*>(q + (left & 4));
+        if (left & 1) one = q[left - 1];
+        const u32x2 rest = has2 ? u32x2{two, one} : u32x2{one, 0};
+        s.w = has4 ? u32x4{four[0], four[1], rest[0], rest[1]} : u32x4{rest[0], rest[1], 0, 0};
       }
     }
   }
@@ -98,10 +114,11 @@ __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const S
       *reinterpret_cast<u32x4_a4*>(q) = s.w;
       *reinterpret_cast<u32x4_a4*>(q + 4) = s.w2;
     } else if constexpr (TAIL) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i < left) q[i] = __uint_as_float(s.w[i]);
-        if (i + 4 < left) q[i + 4] = __uint_as_float(s.w2[i]);
+      if (left > 0) {
+        const u32x4 rest = (left & 4) ? s.w2 : s.w;
+        if (left & 4) *reinterpret_cast<u32x4_a4*>(q) = s.w;
+        if (left & 2) *reinterpret_cast<u32x2_a4*>(q + (left & 4)) = u32x2{rest[0], rest[1]};
+        if (left & 1) q[left - 1] = __uint_as_float((left & 2) ? rest[2] : rest[0]);
       }
     }
   } else {
@@ -109,10 +126,11 @@ __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const S
     if (left >= kSlot) {
       *reinterpret_cast<u32x4_a2*>(q) = s.w;
     } else if constexpr (TAIL) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (2 * i < left) q[2 * i] = (bf16_t)s.w[i];
-        if (2 * i + 1 < left) q[2 * i + 1] = (bf16_t)(s.w[i] >> 16);
+      if (left > 0) {
+        const uint32_t r0 = (left & 4) ? s.w[2] : s.w[0], r1 = (left & 4) ? s.w[3] : s.w[1];
+        if (left & 4) *reinterpret_cast<u32x2_a2*>(q) = u32x2{s.w[0], s.w[1]};
+        if (left & 2) *reinterpret_cast<u32_a2*>(q + (left & 4)) = r0;
+        if (left & 1) q[left - 1] = (bf16_t)((left & 2) ? r1 : r0);
       }
     }
   }
