@@ -49,77 +49,101 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], float (*lds)[16][NV], i
 
 __device__ __forceinline__ float rms_inverse(float sum, int d, float eps) { return 1.0f / sqrtf(sum / d + eps); }
 
-// One row per team of blockDim.x threads (whole waves); VPT slots per thread.
-template <bool AF32, bool RF32, int VPT>
-__global__ void __launch_bounds__(1024) block_norm_kernel(BlockNorm p) {
+// A slot of an fp32 vector, ones where the vector is missing.
+template <bool TAIL>
+__device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, float (&out)[kSlot]) {
+  if (v) {
+    unpack_slot<true>(load_slot<true, TAIL>(v, e, left), out);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kSlot; ++i) out[i] = 1.0f;
+  }
+}
+
+// Teams of blockDim.x threads (whole waves), blockDim.y of them in a
+// workgroup, VPT slots of a row per thread.  Team b takes the rows b, b + n,
+// ... of n teams, all teams of a workgroup in step, so that one barrier
+// serves them.  w_pre and c = beta gate w_post stay in the threads' registers
+// (MANY, several gate rows: c without the gate, whose row is read each time):
+// read anew for every row they would be 12 bytes a channel from L2 beside the
+// row's 8 bytes from memory.  TAIL: d is not a multiple of the slot.
+template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
+__global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(BlockNorm p) {
   __shared__ float lds[2][16][1];
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (t >= p.T) return;  // several teams only where each is one wave: no barrier below
-  const int waves = blockDim.x / 64;
+  const int waves = blockDim.x / 64, d = p.d;
+  const int64_t teams = (int64_t)gridDim.x * blockDim.y;
   int phase = 0;
-  float z[VPT][kSlot], v[kSlot], sum[1] = {0.0f};
-  Slot<RF32> xs[VPT];
+  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
+  float w_pre[VPT][kSlot], c[VPT][kSlot];
 #pragma unroll
   for (int q = 0; q < VPT; ++q) {
-    const int c = (q * blockDim.x + threadIdx.x) * kSlot;
-    if (p.x) xs[q] = load_slot<RF32>(p.x, t * p.d + c, p.d - c);
-    if (p.y) {
-      unpack_slot<AF32>(load_slot<AF32>(p.y, t * p.d + c, p.d - c), z[q]);
+    const int e = column(q), left = d - e;
+    float v[kSlot];
+    load_vec<TAIL>(p.w_pre, e, left, w_pre[q]);
+    load_vec<TAIL>(p.w_post, e, left, c[q]);
+    load_vec<TAIL>(MANY ? nullptr : p.gate, e, left, v);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
-    }
+    for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * v[i];
   }
-  float r = 1.0f;
-  if (p.post_norm) {
-    team_sum<1>(sum, lds, waves, phase);
-    r = rms_inverse(sum[0], p.d, p.eps);
-    if (p.r_post && threadIdx.x == 0) p.r_post[t] = r;
-  }
-  sum[0] = 0.0f;
-  const int64_t g = p.gate ? t / p.gate_every : 0;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.y;
+  for (int64_t t0 = first; t0 < p.T; t0 += teams) {
+    const int64_t t = uniform_i64(t0 + threadIdx.y);
+    const bool on = t < p.T;
+    float z[VPT][kSlot], v[kSlot], sum[1] = {0.0f}, r = 1.0f;
+    Slot<RF32> xs[VPT];
+    if (on) {
 #pragma unroll
-  for (int q = 0; q < VPT; ++q) {
-    const int c = (q * blockDim.x + threadIdx.x) * kSlot;
-    if (p.y) {
-      if (p.post_norm) {
+      for (int q = 0; q < VPT; ++q) {
+        const int left = d - column(q);
+        const int64_t e = t * d + column(q);
+        xs[q] = load_slot<RF32, TAIL>(p.x, e, left);
+        if (p.y) {
+          unpack_slot<AF32>(load_slot<AF32, TAIL>(p.y, e, left), z[q]);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) z[q][i] *= r;
-        if (p.w_post) {
-          unpack_slot<true>(load_slot<true>(p.w_post, c, p.d - c), v);
-#pragma unroll
-          for (int i = 0; i < kSlot; ++i) z[q][i] *= v[i];
+          for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
         }
       }
-      if (p.gate) {
-        unpack_slot<true>(load_slot<true>(p.gate, g * p.d + c, p.d - c), v);
+    }
+    if (p.post_norm) {
+      team_sum<1>(sum, lds, waves, phase);
+      r = rms_inverse(sum[0], d, p.eps);
+      if (on && p.r_post && threadIdx.x == 0) p.r_post[t] = r;
+    }
+    sum[0] = 0.0f;
+    if (on) {
+      const int64_t g = MANY ? t / p.gate_every : 0;
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) z[q][i] *= v[i];
+      for (int q = 0; q < VPT; ++q) {
+        const int left = d - column(q);
+        const int64_t e = t * d + column(q);
+        if (p.y) {
+          if constexpr (MANY) {
+            load_vec<TAIL>(p.gate, g * d + column(q), left, v);
+#pragma unroll
+            for (int i = 0; i < kSlot; ++i) z[q][i] *= v[i];
+          }
+          unpack_slot<RF32>(xs[q], v);
+#pragma unroll
+          for (int i = 0; i < kSlot; ++i) z[q][i] = fmaf(p.alpha, v[i], c[q][i] * (z[q][i] * r));
+          store_slot<RF32, TAIL>(p.x_out, e, left, pack_slot<RF32>(z[q]));
+        } else {
+          unpack_slot<RF32>(xs[q], z[q]);
+        }
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
       }
-      unpack_slot<RF32>(xs[q], v);
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) z[q][i] = fmaf(p.alpha, v[i], p.beta * z[q][i]);
-      store_slot<RF32>(p.x_out, t * p.d + c, p.d - c, pack_slot<RF32>(z[q]));
-    } else {
-      unpack_slot<RF32>(xs[q], z[q]);
     }
+    if (!p.a) continue;
+    team_sum<1>(sum, lds, waves, phase);
+    if (!on) continue;
+    r = rms_inverse(sum[0], d, p.eps);
+    if (p.r_pre && threadIdx.x == 0) p.r_pre[t] = r;
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
-  }
-  if (!p.a) return;
-  team_sum<1>(sum, lds, waves, phase);
-  r = rms_inverse(sum[0], p.d, p.eps);
-  if (p.r_pre && threadIdx.x == 0) p.r_pre[t] = r;
+    for (int q = 0; q < VPT; ++q) {
 #pragma unroll
-  for (int q = 0; q < VPT; ++q) {
-    const int c = (q * blockDim.x + threadIdx.x) * kSlot;
-#pragma unroll
-    for (int i = 0; i < kSlot; ++i) z[q][i] *= r;
-    if (p.w_pre) {
-      unpack_slot<true>(load_slot<true>(p.w_pre, c, p.d - c), v);
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) z[q][i] *= v[i];
+      for (int i = 0; i < kSlot; ++i) z[q][i] *= r * w_pre[q][i];
+      store_slot<AF32, TAIL>(p.a, t * d + column(q), d - column(q), pack_slot<AF32>(z[q]));
     }
-    store_slot<AF32>(p.a, t * p.d + c, p.d - c, pack_slot<AF32>(z[q]));
   }
 }
 
@@ -143,9 +167,8 @@ struct BwdRow {
 // and one that begins here and goes on to row 2b + 1.  The teams' column sums
 // are added over the workgroup and left as its row of part_pre and part_post
 // (A where there is one gate row); sum_parts_kernel adds those rows.
-// The next row's loads are in flight while a row is worked on (PREFETCH).
 // MANY: several gate rows.  TAIL: d is not a multiple of the slot.
-template <bool AF32, bool RF32, int VPT, bool PREFETCH, bool MANY, bool TAIL>
+template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   __shared__ float red[2][16][3];
   __shared__ float cols[1024 * kSlot];
@@ -157,20 +180,12 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   float acc_pre[VPT][kSlot] = {}, acc_a[VPT][kSlot] = {}, acc_post[VPT][kSlot] = {};  // acc_post: MANY only
 
   auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
-  auto vec = [&](const float* v, int64_t e, int left, float (&out)[kSlot]) {
-    if (v) {
-      unpack_slot<true>(load_slot<true, TAIL>(v, e, left), out);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kSlot; ++i) out[i] = 1.0f;
-    }
-  };
   auto load_c = [&](int64_t g) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       float gt[kSlot];
-      vec(p.w_post, column(q), d - column(q), c[q]);
-      vec(p.gate, g * d + column(q), d - column(q), gt);
+      load_vec<TAIL>(p.w_post, column(q), d - column(q), c[q]);
+      load_vec<TAIL>(p.gate, g * d + column(q), d - column(q), gt);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * gt[i];
     }
@@ -181,10 +196,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
     for (int q = 0; q < VPT; ++q) {
       const int left = d - column(q);
       const int64_t e = t * d + column(q);
-      r.x[q] = p.da ? load_slot<RF32, TAIL>(p.x_out, e, left) : Slot<RF32>{};
-      r.a[q] = p.da ? load_slot<AF32, TAIL>(p.da, e, left) : Slot<AF32>{};
-      r.d[q] = p.dx_out ? load_slot<RF32, TAIL>(p.dx_out, e, left) : Slot<RF32>{};
-      r.y[q] = p.y ? load_slot<AF32, TAIL>(p.y, e, left) : Slot<AF32>{};
+      r.x[q] = p.da ? load_slot<RF32, TAIL, true>(p.x_out, e, left) : Slot<RF32>{};
+      r.a[q] = p.da ? load_slot<AF32, TAIL, true>(p.da, e, left) : Slot<AF32>{};
+      r.d[q] = p.dx_out ? load_slot<RF32, TAIL, true>(p.dx_out, e, left) : Slot<RF32>{};
+      r.y[q] = p.y ? load_slot<AF32, TAIL, true>(p.y, e, left) : Slot<AF32>{};
     }
   };
   // One row (t < t1: an idle team only joins the exchange).
@@ -232,14 +247,14 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
         dz[q][i] = fmaf(-m2, xh[q][i], dz[q][i]);
         out[i] = p.y ? p.alpha * dz[q][i] : dz[q][i];
       }
-      store_slot<RF32, TAIL>(p.dx, e, left, pack_slot<RF32>(out));
+      store_slot<RF32, TAIL, true>(p.dx, e, left, pack_slot<RF32>(out));
       if (!p.y) continue;
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
         acc_a[q][i] = fmaf(dz[q][i], yh[q][i], acc_a[q][i]);
         out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
       }
-      store_slot<AF32, TAIL>(p.dy, e, left, pack_slot<AF32>(out));
+      store_slot<AF32, TAIL, true>(p.dy, e, left, pack_slot<AF32>(out));
     }
     if constexpr (!MANY) return;
     const bool ends = (t + 1) % p.gate_every == 0 || t + 1 == p.T;
@@ -252,8 +267,8 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       float wp[kSlot], gt[kSlot];
-      vec(p.w_post, column(q), d - column(q), wp);
-      vec(p.gate, g * d + column(q), d - column(q), gt);
+      load_vec<TAIL>(p.w_post, column(q), d - column(q), wp);
+      load_vec<TAIL>(p.gate, g * d + column(q), d - column(q), gt);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
         const float A = p.beta * acc_a[q][i];
@@ -267,25 +282,12 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   };
 
 #pragma unroll
-  for (int q = 0; q < VPT; ++q) vec(p.w_pre, column(q), d - column(q), w_pre[q]);
+  for (int q = 0; q < VPT; ++q) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[q]);
   if (t0 < p.T) load_c(MANY ? t0 / p.gate_every : 0);
-  const int64_t end = t0 + p.per;
-  if constexpr (PREFETCH) {
-    Row r0, r1;
-    if (t0 < t1) load_row(t0, r0);
-    for (int64_t t = t0; t < end; t += 2) {
-      if (t + 1 < t1) load_row(t + 1, r1);
-      step(t, r0);
-      if (t + 1 == end) break;
-      if (t + 2 < t1) load_row(t + 2, r0);
-      step(t + 1, r1);
-    }
-  } else {
-    for (int64_t t = t0; t < end; ++t) {
-      Row r;
-      if (t < t1) load_row(t, r);
-      step(t, r);
-    }
+  for (int64_t t = t0; t < t0 + p.per; ++t) {
+    Row r;
+    if (t < t1) load_row(t, r);
+    step(t, r);
   }
 
   // Column sums over the workgroup's teams, in team order.
@@ -378,12 +380,21 @@ int team_threads(int d, int vpt) { return (int)ceil_div(ceil_div(d, kSlot * vpt)
 
 template <bool AF32, bool RF32>
 void launch_fwd(const BlockNorm& p, hipStream_t s) {
-  const int vpt = p.d <= 1024 * kSlot ? 1 : 2, th = team_threads(p.d, vpt), teams = th == 64 ? 4 : 1;
-  const dim3 grid((unsigned)ceil_div(p.T, teams)), block(th, teams);
-  if (vpt == 1)
-    block_norm_kernel<AF32, RF32, 1><<<grid, block, 0, s>>>(p);
-  else
-    block_norm_kernel<AF32, RF32, 2><<<grid, block, 0, s>>>(p);
+  constexpr int64_t kGroups = 512;  // two workgroups of 16 waves per compute unit
+  const int vpt = p.d <= 1024 * kSlot ? 1 : 2, th = team_threads(p.d, vpt), tpb = 1024 / th;
+  const int64_t groups = ceil_div(p.T, tpb);
+  auto go = [&](auto kernel) {
+    kernel<<<dim3((unsigned)(groups < kGroups ? groups : kGroups)), dim3(th, tpb), 0, s>>>(p);
+  };
+  const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
+  if (vpt == 1) {
+    if (many)
+      go(tail ? block_norm_kernel<AF32, RF32, 1, true, true> : block_norm_kernel<AF32, RF32, 1, true, false>);
+    else
+      go(tail ? block_norm_kernel<AF32, RF32, 1, false, true> : block_norm_kernel<AF32, RF32, 1, false, false>);
+  } else {
+    go(many ? block_norm_kernel<AF32, RF32, 2, true, true> : block_norm_kernel<AF32, RF32, 2, false, true>);
+  }
 }
 
 // The backward's workgroups: up to 16 waves, one workgroup per compute unit.
@@ -409,14 +420,14 @@ void launch_bwd(const BlockNormBwd& p, const BwdShape& b, hipStream_t s) {
   const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
   if (b.vpt == 1) {
     if (many)
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !RF32, true, true>
-              : block_norm_bwd_kernel<AF32, RF32, 1, !RF32, true, false>);
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, true, true>
+              : block_norm_bwd_kernel<AF32, RF32, 1, true, false>);
     else
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, true>
-              : block_norm_bwd_kernel<AF32, RF32, 1, !AF32, false, false>);
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, false, true>
+              : block_norm_bwd_kernel<AF32, RF32, 1, false, false>);
   } else {
-    go(many ? block_norm_bwd_kernel<AF32, RF32, 2, false, true, true>
-            : block_norm_bwd_kernel<AF32, RF32, 2, false, false, true>);
+    go(many ? block_norm_bwd_kernel<AF32, RF32, 2, true, true>
+            : block_norm_bwd_kernel<AF32, RF32, 2, false, true>);
   }
 }
 

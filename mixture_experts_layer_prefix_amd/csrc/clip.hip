@@ -51,7 +51,7 @@ __device__ __forceinline__ double chunk_squares(const void* p, int64_t e0, int64
   double s = 0.0;
   float v[kSlot];
   for (int c = threadIdx.x * kSlot; c < n; c += 256 * kSlot) {
-    unpack_slot<F32>(load_slot<F32>(p, e0 + c, n - c), v);
+    unpack_slot<F32>(load_slot<F32, true, true>(p, e0 + c, n - c), v);
 #pragma unroll
     for (int i = 0; i < kSlot; ++i) s = fma((double)v[i], (double)v[i], s);
   }

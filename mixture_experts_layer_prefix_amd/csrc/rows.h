@@ -29,18 +29,49 @@ struct Slot<true> {
   u32x4 w, w2;
 };
 
+// 16 bytes at an element's address.
+template <bool NT>
+__device__ __forceinline__ u32x4 get16(const float* p) {
+  const u32x4_a4* q = reinterpret_cast<const u32x4_a4*>(p);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  return *q;
+}
+template <bool NT>
+__device__ __forceinline__ u32x4 get16(const bf16_t* p) {
+  const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+  if constexpr (NT) return __builtin_nontemporal_load(q);
+  return *q;
+}
+template <bool NT>
+__device__ __forceinline__ void put16(float* p, u32x4 v) {
+  u32x4_a4* q = reinterpret_cast<u32x4_a4*>(p);
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
+}
+template <bool NT>
+__device__ __forceinline__ void put16(bf16_t* p, u32x4 v) {
+  u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
+  if constexpr (NT)
+    __builtin_nontemporal_store(v, q);
+  else
+    *q = v;
+}
+
 // Elements [0, left) of the slot at element `e` of p; the others read as 0.
 // TAIL false: the row is whole slots, so left is at least 8 or not positive.
+// NT: whole slots with the streaming hint, for data that is not read again.
 // A partial slot is read and written in pieces of four, two and one elements
 // (one access per bit of left), which the value is shifted together from.
-template <bool F32, bool TAIL = true>
+template <bool F32, bool TAIL = true, bool NT = false>
 __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int left) {
   Slot<F32> s = {};
   if constexpr (F32) {
     const float* q = static_cast<const float*>(p) + e;
     if (left >= kSlot) {
-      s.w = *reinterpret_cast<const u32x4_a4*>(q);
-      s.w2 = *reinterpret_cast<const u32x4_a4*>(q + 4);
+      s.w = get16<NT>(q);
+      s.w2 = get16<NT>(q + 4);
     } else if constexpr (TAIL) {
       if (left > 0) {
         const bool has4 = left & 4, has2 = left & 2;
@@ -58,7 +89,7 @@ __device__ __forceinline__ Slot<F32> load_slot(const void* p, int64_t e, int lef
   } else {
     const bf16_t* q = static_cast<const bf16_t*>(p) + e;
     if (left >= kSlot) {
-      s.w = *reinterpret_cast<const u32x4_a2*>(q);
+      s.w = get16<NT>(q);
     } else if constexpr (TAIL) {
       if (left > 0) {
         const bool has4 = left & 4, has2 = left & 2;
@@ -106,13 +137,13 @@ __device__ __forceinline__ Slot<F32> pack_slot(const float (&v)[kSlot]) {
 }
 
 // Writes elements [0, left) of the slot.
-template <bool F32, bool TAIL = true>
+template <bool F32, bool TAIL = true, bool NT = false>
 __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const Slot<F32>& s) {
   if constexpr (F32) {
     float* q = static_cast<float*>(p) + e;
     if (left >= kSlot) {
-      *reinterpret_cast<u32x4_a4*>(q) = s.w;
-      *reinterpret_cast<u32x4_a4*>(q + 4) = s.w2;
+      put16<NT>(q, s.w);
+      put16<NT>(q + 4, s.w2);
     } else if constexpr (TAIL) {
       if (left > 0) {
         const u32x4 rest = (left & 4) ? s.w2 : s.w;
@@ -124,7 +155,7 @@ __device__ __forceinline__ void store_slot(void* p, int64_t e, int left, const S
   } else {
     bf16_t* q = static_cast<bf16_t*>(p) + e;
     if (left >= kSlot) {
-      *reinterpret_cast<u32x4_a2*>(q) = s.w;
+      put16<NT>(q, s.w);
     } else if constexpr (TAIL) {
       if (left > 0) {
         const uint32_t r0 = (left & 4) ? s.w[2] : s.w[0], r1 = (left & 4) ? s.w[3] : s.w[1];

@@ -152,91 +152,124 @@ RowShape row_shape(int64_t T, int d) {
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
 }
 
-template <bool F32>
+constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
+
+template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
                                                          const int32_t* __restrict__ token_row, void* __restrict__ xp,
                                                          int64_t T, int k, int d) {
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;
   for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
-    const Slot<F32> s = load_slot<F32>(x, t * d + c, d - c);
+    const Slot<F32> s = load_slot<F32, TAIL>(x, t * d + c, d - c);
     for (int j = 0; j < k; ++j) {
       const int64_t row = token_row[t * k + j];
-      if (row_here(row, T * k)) store_slot<F32>(xp, row * d + c, d - c, s);
+      if (row_here(row, T * k)) store_slot<F32, TAIL>(xp, row * d + c, d - c, s);
     }
   }
 }
 
 // y[t] = sum_j w_j rows[row_j] + add[t]; w NULL: every weight 1, add NULL: 0.
 // add may be y: a slot is read before the thread that read it writes it.
-template <bool F32>
+template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ rows,
                                                       const int32_t* __restrict__ token_row,
                                                       const float* __restrict__ w, const void* add, void* y, int64_t T,
                                                       int k, int d) {
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;
+  const int32_t* tr = token_row + t * k;
   for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
     float acc[kSlot] = {}, v[kSlot];
-    for (int j = 0; j < k; ++j) {
-      const int64_t row = token_row[t * k + j];
-      if (!row_here(row, T * k)) continue;
-      const float g = w ? w[t * k + j] : 1.0f;
-      unpack_slot<F32>(load_slot<F32>(rows, row * d + c, d - c), v);
+    Slot<F32> a;
+    if (add) a = load_slot<F32, TAIL>(add, t * d + c, d - c);
+    for (int j0 = 0; j0 < k; j0 += kRoutes) {
+      Slot<F32> s[kRoutes];
+      bool here[kRoutes];
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+      for (int j = 0; j < kRoutes; ++j) {
+        const int64_t row = j0 + j < k ? tr[j0 + j] : -1;
+        here[j] = row_here(row, T * k);
+        if (here[j]) s[j] = load_slot<F32, TAIL>(rows, row * d + c, d - c);
+      }
+#pragma unroll
+      for (int j = 0; j < kRoutes; ++j) {
+        if (!here[j]) continue;
+        const float g = w ? w[t * k + j0 + j] : 1.0f;
+        unpack_slot<F32>(s[j], v);
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+      }
     }
     if (add) {
-      unpack_slot<F32>(load_slot<F32>(add, t * d + c, d - c), v);
+      unpack_slot<F32>(a, v);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) acc[i] += v[i];
     }
-    store_slot<F32>(y, t * d + c, d - c, pack_slot<F32>(acc));
+    store_slot<F32, TAIL>(y, t * d + c, d - c, pack_slot<F32>(acc));
   }
 }
 
-template <bool F32>
+// Weights (dov) and rows of o (dw) are read only for the output they serve.
+template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ o,
                                                           const int32_t* __restrict__ token_row,
                                                           const float* __restrict__ w, void* __restrict__ dov,
                                                           float* __restrict__ dw, int64_t T, int k, int d) {
-  __shared__ float part[16];
-  const int64_t t = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  __shared__ float part[16][16];
+  const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;  // several tokens only where each is one wave: no barrier below
-  const int waves = blockDim.x / 64;
-  for (int j = 0; j < k; ++j) {
-    const int64_t row = token_row[t * k + j];
-    if (!row_here(row, T * k)) {
-      if (dw && threadIdx.x == 0) dw[t * k + j] = 0.0f;
-      continue;
-    }
-    const float g = dov ? w[t * k + j] : 0.0f;  // the weights may be missing where only dw is wanted
-    float dot = 0.0f, a[kSlot], b[kSlot];
+  const int waves = blockDim.x / 64, lane = threadIdx.x & 63;
+  const int32_t* tr = token_row + t * k;
+  for (int j0 = 0; j0 < k; j0 += kRoutes) {
+    float dot[kRoutes] = {};
     for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
-      unpack_slot<F32>(load_slot<F32>(dy, t * d + c, d - c), a);
-      if (dw) {
-        unpack_slot<F32>(load_slot<F32>(o, row * d + c, d - c), b);
+      float a[kSlot], b[kSlot];
+      const Slot<F32> q = load_slot<F32, TAIL>(dy, t * d + c, d - c);
+      Slot<F32> s[kRoutes];
+      int64_t row[kRoutes];
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) dot = fmaf(a[i], b[i], dot);
+      for (int j = 0; j < kRoutes; ++j) {
+        row[j] = j0 + j < k ? tr[j0 + j] : -1;
+        if (dw && row_here(row[j], T * k)) s[j] = load_slot<F32, TAIL, true>(o, row[j] * d + c, d - c);
       }
-      if (dov) {
+      unpack_slot<F32>(q, a);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) b[i] = g * a[i];
-        store_slot<F32>(dov, row * d + c, d - c, pack_slot<F32>(b));
+      for (int j = 0; j < kRoutes; ++j) {
+        if (!row_here(row[j], T * k)) continue;
+        if (dw) {
+          unpack_slot<F32>(s[j], b);
+#pragma unroll
+          for (int i = 0; i < kSlot; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
+        }
+        if (dov) {
+          const float g = w[t * k + j0 + j];
+#pragma unroll
+          for (int i = 0; i < kSlot; ++i) b[i] = g * a[i];
+          store_slot<F32, TAIL>(dov, row[j] * d + c, d - c, pack_slot<F32>(b));
+        }
       }
     }
     if (!dw) continue;
-    dot = wave_sum(dot);
-    if (waves > 1) {
-      if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
-      __syncthreads();
-      dot = 0.0f;
-      for (int i = 0; i < waves; ++i) dot += part[i];
-      __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kRoutes; ++j) {
+      dot[j] = wave_sum(dot[j]);  // 0 for an absent route
+      if (waves > 1 && lane == 0) part[threadIdx.x >> 6][j0 + j] = dot[j];
+      if (waves == 1 && lane == 0 && j0 + j < k) dw[t * k + j0 + j] = dot[j];
     }
-    if (threadIdx.x == 0) dw[t * k + j] = dot;
+  }
+  if (!dw || waves == 1) return;
+  __syncthreads();
+  if ((int)threadIdx.x < k) {
+    float v = 0.0f;
+    for (int i = 0; i < waves; ++i) v += part[i][threadIdx.x];
+    dw[t * k + threadIdx.x] = v;
   }
 }
+
+// A kernel's instance for an element type and a row length.
+#define ROW_KERNEL(name, f32, d)                                                  \
+  ((d) % kSlot ? ((f32) ? name<true, true> : name<false, true>) : ((f32) ? name<true, false> : name<false, false>))
 
 }  // namespace
 
@@ -259,7 +292,7 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
   sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
   if (x_perm) {
     const RowShape g = row_shape(T, d);
-    (f32 ? sort_rows_kernel<true> : sort_rows_kernel<false>)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
+    ROW_KERNEL(sort_rows_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
   }
   return hipGetLastError();
 }
@@ -268,7 +301,7 @@ hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, c
                          int64_t T, int d, int k, hipStream_t s) {
   if (T == 0) return hipSuccess;
   const RowShape g = row_shape(T, d);
-  (f32 ? unsort_kernel<true> : unsort_kernel<false>)<<<g.grid, g.block, 0, s>>>(rows, token_row, w, add, y, T, k, d);
+  ROW_KERNEL(unsort_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(rows, token_row, w, add, y, T, k, d);
   return hipGetLastError();
 }
 
@@ -276,8 +309,8 @@ hipError_t launch_unsort_bwd(bool f32, const void* dy, const void* o_perm, const
                              void* do_perm, float* dw, int64_t T, int d, int k, hipStream_t s) {
   if (T == 0) return hipSuccess;
   const RowShape g = row_shape(T, d);
-  (f32 ? unsort_bwd_kernel<true> : unsort_bwd_kernel<false>)<<<g.grid, g.block, 0, s>>>(dy, o_perm, token_row, w,
-                                                                                        do_perm, dw, T, k, d);
+  ROW_KERNEL(unsort_bwd_kernel, f32, d)
+  <<<g.grid, g.block, 0, s>>>(dy, o_perm, token_row, w, do_perm, dw, T, k, d);
   return hipGetLastError();
 }
 
