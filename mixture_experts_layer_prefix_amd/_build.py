@@ -1,5 +1,6 @@
-"""Build step of the HIP library: compiles csrc/*.hip and csrc/*.cpp for
-gfx950 with hipcc and links libmoe.so next to this file."""
+"""Build step: compiles csrc/*.hip and csrc/*.cpp for gfx950 with hipcc and
+links libmoe.so next to this file, and compiles the Python wrappers' helper
+module _tensors (binding/tensors.cpp, host code against torch's headers)."""
 import concurrent.futures as cf
 import os
 import subprocess
@@ -8,6 +9,8 @@ _DIR = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(_DIR, "csrc")
 BUILD = os.path.join(_DIR, "_build")
 LIB = os.path.join(_DIR, "libmoe.so")
+BINDING = os.path.join(_DIR, "binding", "tensors.cpp")
+BINDING_LIB = os.path.join(_DIR, "_tensors.so")
 FLAGS = ["-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC", "-Wall", "-Wno-unused-function",
          "-Wno-pass-failed", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
@@ -27,10 +30,29 @@ def _compile(src):
     return obj, warn
 
 
+def _compile_binding():
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING_LIB + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + sysconfig.get_paths()["include"]]
+    for p in include_paths():
+        cmd += ["-isystem", p]
+    cmd += [BINDING, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s" % (" ".join(cmd), r.stderr))
+    os.replace(tmp, BINDING_LIB)
+
+
 def build(verbose=False, jobs=8):
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(_compile, sources()))
+        binding.result()
     if verbose:
         for obj, warn in results:
             if warn:

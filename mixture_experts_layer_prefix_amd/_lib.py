@@ -113,6 +113,21 @@ def lib():
     return _lib
 
 
+_tensors_module = None
+
+
+def tensors():
+    """The helper module _tensors (raises if it has not been built)."""
+    global _tensors_module
+    if _tensors_module is None:
+        if not os.path.exists(os.path.join(_DIR, "_tensors.so")):
+            raise RuntimeError("_tensors.so not found in %s: build it with __graft_entry__.build()" % _DIR)
+        import torch  # noqa: F401  (its libraries first)
+        from . import _tensors
+        _tensors_module = _tensors
+    return _tensors_module
+
+
 def status_str(code):
     return lib().moe_status_str(code).decode()
 

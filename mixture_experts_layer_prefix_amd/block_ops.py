@@ -3,7 +3,6 @@ sorted by expert and back, the norms before and after a residual block, and
 gradient clipping.  They check their tensors, allocate outputs and workspaces
 with torch and pass pointers and the stream that is current on the tensors'
 device; no arithmetic happens here."""
-import array
 import contextlib
 import ctypes
 from dataclasses import dataclass
@@ -28,11 +27,12 @@ def _check(name, t, dtype, shape, device):
     type and shape on this device.  None: a null pointer."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    p = _lib.tensors().address(t, dtype, shape, device.index)
+    if p < 0:
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s" % (
-            name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+            name, dtype, shape, device, t.dtype, tuple(t.shape), t.device,
             "" if t.is_contiguous() else " (not contiguous)"))
-    return t.data_ptr()
+    return p
 
 
 def _need(name, t):
@@ -43,15 +43,18 @@ def _need(name, t):
     return t.device
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """Makes `device` current around a launch (its streams, its kernels)."""
-    if torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    """The stream current on `device`, as torch.cuda.current_stream(device)
+    gives it, without making a Stream object (1 us) for each call."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _device(device):
@@ -286,38 +289,29 @@ def block_norm_backward(block: Block, dx_out, da, x_out, y, r_pre, r_post, w_pre
 
 
 # ---- gradient norm and clipping --------------------------------------------
-_TYPE = {torch.float32: PREC["f32"], torch.bfloat16: PREC["bf16"]}
-
-
 def _tensors(name, tensors):
-    """Host arrays (addresses, element counts, types) of a list of tensors."""
-    ptrs, numel, types = array.array("Q"), array.array("q"), array.array("i")
-    device = None
-    for i, t in enumerate(tensors):
-        if t.dtype not in _TYPE or not t.is_contiguous() or t.device != (device or _need(name, t)):
-            raise ValueError("%s[%d] must be a contiguous bf16 or fp32 tensor on the device of the others" % (name, i))
-        device = t.device
-        ptrs.append(t.data_ptr())
-        numel.append(t.numel())
-        types.append(_TYPE[t.dtype])
-    return ptrs, numel, types, device
+    """Host arrays (addresses, element counts, types) of a list of tensors,
+    and their device."""
+    got = _lib.tensors().describe(tensors)
+    if isinstance(got, int):
+        raise ValueError("%s[%d] must be a contiguous bf16 or fp32 tensor on the GPU of the others" % (name, got))
+    if got[3] < 0:
+        raise ValueError("%s holds no tensor" % name)
+    return got[0], got[1], got[2], torch.device("cuda", got[3])
 
 
-def _scratch(numel, device):
-    n = _lib.lib().moe_grad_norm_scratch_bytes(numel.buffer_info()[0], len(numel))
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device), n
+def _scratch(numel, n, device):
+    size = _lib.lib().moe_grad_norm_scratch_bytes(numel, n)
+    return torch.empty(max(size, 16), dtype=torch.uint8, device=device), size
 
 
 def grad_norm(grads):
     """moe_grad_norm: the norm over all tensors, fp32 [1] on their device."""
     ptrs, numel, types, dev = _tensors("grads", grads)
-    if dev is None:
-        raise ValueError("grads holds no tensor")
     norm = torch.empty(1, dtype=torch.float32, device=dev)
-    ws, n = _scratch(numel, dev)
+    ws, size = _scratch(numel, len(grads), dev)
     with _on(dev):
-        call("moe_grad_norm", ptrs.buffer_info()[0], numel.buffer_info()[0], types.buffer_info()[0], len(ptrs),
-             norm.data_ptr(), ws.data_ptr(), n, _stream(dev))
+        call("moe_grad_norm", ptrs, numel, types, len(grads), norm.data_ptr(), ws.data_ptr(), size, _stream(dev))
     return norm
 
 
@@ -327,23 +321,20 @@ def clip_grads(grads, max_norm, norm=None, out=None):
     (fp32 [1]): the norm to clip by, for instance one joined over ranks; None:
     that of these tensors."""
     ptrs, numel, types, dev = _tensors("grads", grads)
-    if dev is None:
-        raise ValueError("grads holds no tensor")
     optrs = ptrs
     if out is not None:
         optrs, onumel, otypes, odev = _tensors("out", out)
         if onumel != numel or otypes != types or odev != dev:
             raise ValueError("out must match grads in number, size, type and device")
-    if len({p for p, n in zip(optrs, numel) if n}) != sum(1 for n in numel if n):
+    if not _lib.tensors().distinct(optrs, numel):
         raise ValueError("a tensor would be scaled twice: %s holds one more than once" % ("grads" if out is None
                                                                                          else "out"))
     given = _check("norm", norm, torch.float32, (1,), dev)
-    ws, n, ws_ptr = None, 0, None
+    ws, size = None, 0
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
-        ws, n = _scratch(numel, dev)
-        ws_ptr = ws.data_ptr()
+        ws, size = _scratch(numel, len(grads), dev)
     with _on(dev):
-        call("moe_clip_grads", ptrs.buffer_info()[0], optrs.buffer_info()[0], numel.buffer_info()[0],
-             types.buffer_info()[0], len(ptrs), max_norm, given, norm.data_ptr(), ws_ptr, n, _stream(dev))
+        call("moe_clip_grads", ptrs, optrs, numel, types, len(grads), max_norm, given, norm.data_ptr(),
+             None if ws is None else ws.data_ptr(), size, _stream(dev))
     return (grads if out is None else out), norm

@@ -5,7 +5,7 @@
 namespace moe {
 
 constexpr int kChunk = 16384;               // elements a workgroup takes at a time
-constexpr int kClipGroups = 2048;           // workgroups at most
+constexpr int kClipGroups = 1024;           // workgroups at most, four per compute unit
 constexpr int64_t kEntryMax = 1ll << 30;    // elements of one table entry at most (a multiple of kChunk)
 constexpr uint32_t kF32Entry = 0x80000000u; // flag in numel: fp32 elements (bf16 otherwise)
 

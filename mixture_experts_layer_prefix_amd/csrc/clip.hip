@@ -18,18 +18,27 @@ namespace moe {
 
 namespace {
 
-// Entry of chunk c: the last one whose first chunk is at most c.
-__device__ __forceinline__ int find_entry(const uint32_t* first, int n, uint32_t c) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int m = (lo + hi) / 2;
-    if (first[m] <= c)
-      lo = m;
-    else
-      hi = m;
+// A wave's copy of a table's `first`, a few entries per lane, from which the
+// entry of a chunk follows without a chain of loads: the number of entries
+// that start at or before it, less one.
+template <class Table>
+struct EntryIndex {
+  static constexpr int kPer = (Table::kEntries + 63) / 64;
+  uint32_t first[kPer];
+  __device__ explicit EntryIndex(const Table& t) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = i * 64 + (threadIdx.x & 63);
+      first[i] = e < t.n ? t.first[e] : 0xFFFFFFFFu;
+    }
   }
-  return lo;
-}
+  __device__ int find(uint32_t chunk) const {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) n += __popcll(__ballot(first[i] <= chunk));
+    return n - 1;
+  }
+};
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
 #pragma unroll
@@ -45,24 +54,42 @@ __device__ __forceinline__ double group_sum_f64(double v, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
+constexpr int kBatch = 4;  // slots a thread has in flight
+
+// Calls f(element, elements left, batch of slots) for the chunk's slots of
+// this thread, kBatch at a time; whole slots first, without bounds.
+template <bool F32, class F>
+__device__ __forceinline__ void for_slots(const void* src, int64_t e0, int n, F f) {
+  constexpr int kStep = 256 * kSlot;
+  int c = threadIdx.x * kSlot;
+  for (; c + (kBatch - 1) * kStep + kSlot <= n; c += kBatch * kStep) {
+    Slot<F32> s[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) s[i] = load_slot<F32, false, true>(src, e0 + c + i * kStep, kSlot);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) f(e0 + c + i * kStep, kSlot, s[i]);
+  }
+  for (; c < n; c += kStep) f(e0 + c, n - c, load_slot<F32, true, true>(src, e0 + c, n - c));
+}
+
 template <bool F32>
 __device__ __forceinline__ double chunk_squares(const void* p, int64_t e0, int64_t numel) {
-  const int n = (int)min((int64_t)kChunk, numel - e0);
   double s = 0.0;
-  float v[kSlot];
-  for (int c = threadIdx.x * kSlot; c < n; c += 256 * kSlot) {
-    unpack_slot<F32>(load_slot<F32, true, true>(p, e0 + c, n - c), v);
+  for_slots<F32>(p, e0, (int)min((int64_t)kChunk, numel - e0), [&](int64_t, int, const Slot<F32>& q) {
+    float v[kSlot];
+    unpack_slot<F32>(q, v);
 #pragma unroll
     for (int i = 0; i < kSlot; ++i) s = fma((double)v[i], (double)v[i], s);
-  }
+  });
   return s;
 }
 
 __global__ void __launch_bounds__(256) squares_kernel(NormTable t, double* __restrict__ part) {
   __shared__ double lds[4];
+  const EntryIndex<NormTable> index(t);
   double s = 0.0;
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int i = find_entry(t.first, t.n, c);
+    const int i = index.find(c);
     const int64_t e0 = (int64_t)(c - t.first[i]) * kChunk;
     const uint32_t m = t.numel[i];
     s += (m & kF32Entry) ? chunk_squares<true>(t.src[i], e0, m & ~kF32Entry)
@@ -93,14 +120,13 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
 
 template <bool F32>
 __device__ __forceinline__ void scale_chunk(const void* src, void* dst, int64_t e0, int64_t numel, float f) {
-  const int n = (int)min((int64_t)kChunk, numel - e0);
-  float v[kSlot];
-  for (int c = threadIdx.x * kSlot; c < n; c += 256 * kSlot) {
-    unpack_slot<F32>(load_slot<F32>(src, e0 + c, n - c), v);
+  for_slots<F32>(src, e0, (int)min((int64_t)kChunk, numel - e0), [&](int64_t e, int left, const Slot<F32>& q) {
+    float v[kSlot];
+    unpack_slot<F32>(q, v);
 #pragma unroll
     for (int i = 0; i < kSlot; ++i) v[i] *= f;
-    store_slot<F32>(dst, e0 + c, n - c, pack_slot<F32>(v));
-  }
+    store_slot<F32, true, true>(dst, e, left, pack_slot<F32>(v));
+  });
 }
 
 // part null: the norm is *norm_in.
@@ -110,8 +136,9 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double* _
   const float norm = part ? norm_of(part, nparts, lds) : *norm_in;
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
   const float f = clip_factor(norm, max_norm);
+  const EntryIndex<ClipTable> index(t);
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
-    const int i = find_entry(t.first, t.n, c);
+    const int i = index.find(c);
     const int64_t e0 = (int64_t)(c - t.first[i]) * kChunk;
     const uint32_t m = t.numel[i];
     if (m & kF32Entry)

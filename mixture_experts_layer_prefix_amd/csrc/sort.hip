@@ -32,8 +32,9 @@ __global__ void __launch_bounds__(kSortRoutes) sort_count_kernel(const int32_t* 
   for (int i = threadIdx.x; i < E; i += kSortRoutes) block_counts[(int64_t)i * gridDim.x + blockIdx.x] = h[i];
 }
 
-// Exclusive prefix over the threads of a 256-thread workgroup; *total its sum.
-__device__ __forceinline__ int scan256(int v, int* lds, int* total) {
+// Exclusive prefix over the threads of a workgroup (lds: one int per wave);
+// *total its sum.
+__device__ __forceinline__ int scan_threads(int v, int* lds, int* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int inc = v;
 #pragma unroll
@@ -44,8 +45,7 @@ __device__ __forceinline__ int scan256(int v, int* lds, int* total) {
   if (lane == 63) lds[wave] = inc;
   __syncthreads();
   int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) {
     if (w < wave) before += lds[w];
     all += lds[w];
   }
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256) sort_scan_kernel(int32_t* __restrict__ bl
   const int b0 = min((int)threadIdx.x * per, nb), b1 = min(b0 + per, nb);
   int sum = 0, total;
   for (int b = b0; b < b1; ++b) sum += col[b];
-  int run = scan256(sum, lds, &total);
+  int run = scan_threads(sum, lds, &total);
   for (int b = b0; b < b1; ++b) {
     const int c = col[b];
     col[b] = run;
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kSortRoutes) sort_rank_kernel(const int32_t* _
     c[q] = e0 + q < E ? counts[e0 + q] : 0;
     sum += c[q];
   }
-  int run = scan256(sum, lds, &total);
+  int run = scan_threads(sum, lds, &total);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (e0 + q < E) {
@@ -150,6 +150,93 @@ RowShape row_shape(int64_t T, int d) {
   th = th > 1024 ? 1024 : th;
   const int tok = th >= 256 ? 1 : 256 / th;
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
+}
+
+// The whole sort in one launch for a few routes, at the cost of every
+// workgroup reading all the ids: workgroup t < T finds the rows of token t's
+// routes by counting the routes that come before them (an expert below, or
+// the same expert and a smaller route) and copies the token; workgroup T
+// makes the counts and offsets.  At least 256 threads.
+template <bool F32, bool TAIL>
+__global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restrict__ idx, const void* __restrict__ x,
+                                                        int T, int d, int E, int k, int32_t* __restrict__ counts,
+                                                        int32_t* __restrict__ offsets,
+                                                        int32_t* __restrict__ row_token,
+                                                        int32_t* __restrict__ token_row, void* __restrict__ xp) {
+  __shared__ int32_t h[1024];
+  __shared__ int32_t part[16][16];
+  __shared__ int lds[16];
+  const int R = T * k, t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  if (t == T) {
+    for (int e = threadIdx.x; e < 1024; e += blockDim.x) h[e] = 0;
+    __syncthreads();
+    for (int r = threadIdx.x; r < R; r += blockDim.x) {
+      const int e = idx[r];
+      if ((unsigned)e < (unsigned)E) atomicAdd(&h[e], 1);
+    }
+    __syncthreads();
+    const int e0 = threadIdx.x * 4;  // the first 256 threads hold the experts
+    int c[4] = {}, sum = 0, total;
+    if (e0 < 1024) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) sum += c[q] = h[e0 + q];
+    }
+    int run = scan_threads(sum, lds, &total);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (e0 + q < E) {
+        counts[e0 + q] = c[q];
+        offsets[e0 + q] = run;
+      }
+      run += c[q];
+    }
+    if (threadIdx.x == 0) offsets[E] = total;
+    return;
+  }
+  const int r0 = t * k;
+  int c = threadIdx.x * kSlot;  // the token's first slots are under way while the rows are found
+  Slot<F32> s = {};
+  if (xp) s = load_slot<F32, TAIL>(x, (int64_t)t * d + c, d - c);
+  int before[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) before[j] = 0;
+  for (int base = 0; base < R; base += blockDim.x) {
+    const int r = base + threadIdx.x;
+    int e = r < R ? idx[r] : -1;
+    if ((unsigned)e >= (unsigned)E) e = E;  // absent: behind every expert
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (j < k) {
+        const int ej = idx[r0 + j];
+        before[j] += __popcll(__ballot(e < ej || (e == ej && r < r0 + j)));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (lane == j) part[wave][j] = before[j];
+  __syncthreads();
+  if ((int)threadIdx.x < k) {
+    const int e = idx[r0 + threadIdx.x];
+    int row = -1;
+    if ((unsigned)e < (unsigned)E) {
+      row = 0;
+      for (int w = 0; w < waves; ++w) row += part[w][threadIdx.x];
+      row_token[row] = t;
+    }
+    token_row[r0 + threadIdx.x] = row;
+    h[threadIdx.x] = row;
+  }
+  if (!xp) return;
+  __syncthreads();
+  while (c < d) {
+    for (int j = 0; j < k; ++j) {
+      const int row = __builtin_amdgcn_readfirstlane(h[j]);
+      if (row >= 0) store_slot<F32, TAIL>(xp, (int64_t)row * d + c, d - c, s);
+    }
+    c += blockDim.x * kSlot;
+    if (c < d) s = load_slot<F32, TAIL>(x, (int64_t)t * d + c, d - c);
+  }
 }
 
 constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
@@ -273,6 +360,8 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
 
 }  // namespace
 
+constexpr int64_t kFewRoutes = 4096;
+
 size_t sort_scratch_bytes(int64_t T, int k, int E) {
   return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
 }
@@ -285,6 +374,13 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
     return hipGetLastError();
   }
   const int64_t R = T * k;
+  if (R <= kFewRoutes) {
+    const int slots = (int)ceil_div(d, kSlot);
+    const int th = slots <= 256 ? 256 : slots >= 1024 ? 1024 : (slots + 63) / 64 * 64;
+    ROW_KERNEL(sort_few_kernel, f32, d)
+    <<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm);
+    return hipGetLastError();
+  }
   const unsigned nb = (unsigned)ceil_div(R, kSortRoutes);
   int32_t* bc = static_cast<int32_t*>(scratch);
   sort_count_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, bc);
