@@ -146,7 +146,7 @@ struct RowShape {
   dim3 grid, block;
 };
 RowShape row_shape(int64_t T, int d) {
-  int th = (int)ceil_div(ceil_div(d, kSlot * 2), 64) * 64;  // two slots per thread
+  int th = (int)ceil_div(ceil_div(d, kSlot), 64) * 64;  // one slot per thread
   th = th > 1024 ? 1024 : th;
   const int tok = th >= 256 ? 1 : 256 / th;
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
