@@ -130,6 +130,63 @@ __global__ void __launch_bounds__(kSortRoutes) sort_rank_kernel(const int32_t* _
   }
 }
 
+// The schedule in one launch where the ids are few enough for every workgroup
+// to read them all: workgroup b counts, per expert, the routes before its
+// kSortRoutes own ones and the routes from there on.  Their sum is the
+// expert's count, and the first count what its own ranks start from.
+__global__ void __launch_bounds__(1024) sort_wide_kernel(const int32_t* __restrict__ idx, int R, int E, int k,
+                                                                int32_t* __restrict__ counts,
+                                                                int32_t* __restrict__ offsets,
+                                                                int32_t* __restrict__ row_token,
+                                                                int32_t* __restrict__ token_row) {
+  __shared__ int32_t before[1024], after[1024];  // before becomes the experts' next rows
+  __shared__ int lds[16];
+  const int tid = threadIdx.x, lane = tid & 63, r0 = blockIdx.x * kSortRoutes;
+  before[tid] = 0;
+  after[tid] = 0;
+  __syncthreads();
+  auto count = [&](int r, int e) {
+    if ((unsigned)e < (unsigned)E) atomicAdd(r < r0 ? &before[e] : &after[e], 1);
+  };
+  int r = tid * 4;
+#pragma unroll 4
+  for (; r + 4 <= R; r += 1024 * 4) {
+    const u32x4 e = get16<false>(reinterpret_cast<const float*>(idx + r));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count(r + i, (int)e[i]);
+  }
+  for (int i = 0; i < 4; ++i)
+    if (r + i < R) count(r + i, idx[r + i]);
+  __syncthreads();
+  const int all = before[tid] + after[tid];  // of expert tid
+  int total;
+  const int first = scan_threads(all, lds, &total);
+  before[tid] += first;
+  if (blockIdx.x == 0 && tid < E) {
+    counts[tid] = all;
+    offsets[tid] = first;
+    if (tid == 0) offsets[E] = total;
+  }
+  r = r0 + tid;
+  const bool mine = tid < kSortRoutes && r < R;
+  int e = mine ? idx[r] : -1;
+  if ((unsigned)e >= (unsigned)E) e = -1;
+  const uint64_t same = same_id_lanes(e);
+  const int rank = __popcll(same & ((1ull << lane) - 1));
+  int row = -1;
+  for (int w = 0; w < kSortRoutes / 64; ++w) {
+    __syncthreads();
+    if ((tid >> 6) == w && e >= 0) {
+      row = before[e] + rank;
+      if ((same >> lane) == 1) before[e] += __popcll(same);
+    }
+  }
+  if (mine) {
+    token_row[r] = row;
+    if (row >= 0) row_token[row] = r / k;
+  }
+}
+
 __global__ void __launch_bounds__(256) sort_empty_kernel(int32_t* counts, int32_t* offsets, int E) {
   for (int e = threadIdx.x; e <= E; e += 256) {
     if (e < E) counts[e] = 0;
@@ -305,9 +362,11 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
                                                           float* __restrict__ dw, int64_t T, int k, int d) {
   __shared__ float part[16][16];
   const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
-  if (t >= T) return;  // several tokens only where each is one wave: no barrier below
   const int waves = blockDim.x / 64, lane = threadIdx.x & 63;
+  float(*sums)[16] = part + threadIdx.y * waves;  // a row per wave of the token
+  if (t >= T) k = 0;                              // the workgroup's last tokens may be missing
   const int32_t* tr = token_row + t * k;
+  const int64_t R = T * k;
   for (int j0 = 0; j0 < k; j0 += kRoutes) {
     float dot[kRoutes] = {};
     for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
@@ -318,12 +377,12 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
         row[j] = j0 + j < k ? tr[j0 + j] : -1;
-        if (dw && row_here(row[j], T * k)) s[j] = load_slot<F32, TAIL, true>(o, row[j] * d + c, d - c);
+        if (dw && row_here(row[j], R)) s[j] = load_slot<F32, TAIL, true>(o, row[j] * d + c, d - c);
       }
       unpack_slot<F32>(q, a);
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
-        if (!row_here(row[j], T * k)) continue;
+        if (!row_here(row[j], R)) continue;
         if (dw) {
           unpack_slot<F32>(s[j], b);
 #pragma unroll
@@ -341,7 +400,7 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
 #pragma unroll
     for (int j = 0; j < kRoutes; ++j) {
       dot[j] = wave_sum(dot[j]);  // 0 for an absent route
-      if (waves > 1 && lane == 0) part[threadIdx.x >> 6][j0 + j] = dot[j];
+      if (waves > 1 && lane == 0) sums[threadIdx.x >> 6][j0 + j] = dot[j];
       if (waves == 1 && lane == 0 && j0 + j < k) dw[t * k + j0 + j] = dot[j];
     }
   }
@@ -349,7 +408,7 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
   __syncthreads();
   if ((int)threadIdx.x < k) {
     float v = 0.0f;
-    for (int i = 0; i < waves; ++i) v += part[i][threadIdx.x];
+    for (int i = 0; i < waves; ++i) v += sums[i][threadIdx.x];
     dw[t * k + threadIdx.x] = v;
   }
 }
@@ -360,7 +419,14 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
 
 }  // namespace
 
-constexpr int64_t kFewRoutes = 4096;
+// Which schedule: kernel times in us, without the 1 to 2 us between launches,
+// for 256 experts and k = 8; "few" holds the copy of the rows, whose own
+// kernel takes 3.0 (d = 512) to 11.3 (d = 7168, 4,096 routes) beside the others.
+//   routes               512   2,048   4,096   32,768   65,536   131,072
+//   few   d = 512/7168   5/6.4 8.8/10.4 13.9/20.8
+//   wide                 4.6   5.0     5.3     9.0      15.1     20
+//   count, scan, rank    8.6   9.8     10.4    13       15       16
+constexpr int64_t kFewRoutes = 2048, kWideLimit = 65536;
 
 size_t sort_scratch_bytes(int64_t T, int k, int E) {
   return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
@@ -381,11 +447,16 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
     <<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm);
     return hipGetLastError();
   }
-  const unsigned nb = (unsigned)ceil_div(R, kSortRoutes);
-  int32_t* bc = static_cast<int32_t*>(scratch);
-  sort_count_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, bc);
-  sort_scan_kernel<<<(unsigned)E, 256, 0, s>>>(bc, (int)nb, counts);
-  sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
+  if (R <= kWideLimit) {
+    sort_wide_kernel<<<(unsigned)ceil_div(R, kSortRoutes), 1024, 0, s>>>(topk_idx, (int)R, E, k, counts, offsets,
+                                                                         row_token, token_row);
+  } else {
+    const unsigned nb = (unsigned)ceil_div(R, kSortRoutes);
+    int32_t* bc = static_cast<int32_t*>(scratch);
+    sort_count_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, bc);
+    sort_scan_kernel<<<(unsigned)E, 256, 0, s>>>(bc, (int)nb, counts);
+    sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
+  }
   if (x_perm) {
     const RowShape g = row_shape(T, d);
     ROW_KERNEL(sort_rows_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);

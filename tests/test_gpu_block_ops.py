@@ -92,7 +92,8 @@ def test_empty_batch():
 
 # ---- unsort and the gradients ----------------------------------------------
 UNSORT = [(1, 7, 1, "none"), (1, 200, 8, "some"), (5, 33, 4, "some"), (16, 1024, 8, "none"), (33, 8, 16, "some"),
-          (70, 130, 3, "some"), (64, 513, 12, "some"), (20, 4100, 6, "none"), (257, 72, 2, "all"), (12, 9001, 5, "some")]
+          (70, 130, 3, "some"), (64, 513, 12, "some"), (20, 4100, 6, "none"), (257, 72, 2, "all"), (12, 9001, 5, "some"),
+          (37, 1500, 9, "some"), (31, 1024, 8, "some"), (11, 600, 16, "some")]
 
 
 def unsort_inputs(T, d, k, absent, prec, seed):
