@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(Bloc
     }
     sum[0] = 0.0f;
     if (on) {
-      const int64_t g = MANY ? t / p.gate_every : 0;
+      const int64_t g = MANY ? (uint32_t)t / (uint32_t)p.gate_every : 0;  // MANY: fewer than 2^23 tokens
 #pragma unroll
       for (int q = 0; q < VPT; ++q) {
         const int left = d - column(q);
@@ -147,9 +147,10 @@ __global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(Bloc
   }
 }
 
-// The raw slots of one row: x', da, dx', y.
+// The raw slots of one row: x', da, dx', y; and its r_pre and r_post.
 template <bool AF32, bool RF32, int VPT>
 struct BwdRow {
+  float r2, r1;
   Slot<RF32> x[VPT], d[VPT];
   Slot<AF32> a[VPT], y[VPT];
 };
@@ -172,44 +173,44 @@ template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   __shared__ float red[2][16][3];
   __shared__ float cols[1024 * kSlot];
-  const int64_t b = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t t0 = b * p.per, t1 = min(t0 + p.per, p.T);
+  const int b = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
+  const int T = (int)p.T, per = (int)p.per, every = MANY ? (int)p.gate_every : T;
+  const int t0 = min(b * per, T), t1 = min(t0 + per, T);
   const int waves = blockDim.x / 64, d = p.d;
   int phase = 0;
+  int g = MANY ? t0 / every : 0, g_end = min((g + 1) * every, T);  // the row's gate group and its end
   float w_pre[VPT][kSlot], c[VPT][kSlot];
   float acc_pre[VPT][kSlot] = {}, acc_a[VPT][kSlot] = {}, acc_post[VPT][kSlot] = {};  // acc_post: MANY only
 
   auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
-  auto load_c = [&](int64_t g) {
+  auto load_c = [&] {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       float gt[kSlot];
       load_vec<TAIL>(p.w_post, column(q), d - column(q), c[q]);
-      load_vec<TAIL>(p.gate, g * d + column(q), d - column(q), gt);
+      load_vec<TAIL>(p.gate, (int64_t)g * d + column(q), d - column(q), gt);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * gt[i];
     }
   };
   typedef BwdRow<AF32, RF32, VPT> Row;
-  auto load_row = [&](int64_t t, Row& r) {
+  auto load_row = [&](int t, Row& r) {
+    r.r2 = p.da ? p.r_pre[t] : 0.0f;
+    r.r1 = p.post_norm ? p.r_post[t] : 1.0f;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       const int left = d - column(q);
-      const int64_t e = t * d + column(q);
-      r.x[q] = p.da ? load_slot<RF32, TAIL, true>(p.x_out, e, left) : Slot<RF32>{};
-      r.a[q] = p.da ? load_slot<AF32, TAIL, true>(p.da, e, left) : Slot<AF32>{};
-      r.d[q] = p.dx_out ? load_slot<RF32, TAIL, true>(p.dx_out, e, left) : Slot<RF32>{};
-      r.y[q] = p.y ? load_slot<AF32, TAIL, true>(p.y, e, left) : Slot<AF32>{};
+      const int64_t e = (int64_t)t * d + column(q);
+      r.x[q] = p.da ? load_slot<RF32, TAIL, !RF32>(p.x_out, e, left) : Slot<RF32>{};
+      r.a[q] = p.da ? load_slot<AF32, TAIL, !AF32>(p.da, e, left) : Slot<AF32>{};
+      r.d[q] = p.dx_out ? load_slot<RF32, TAIL, !RF32>(p.dx_out, e, left) : Slot<RF32>{};
+      r.y[q] = p.y ? load_slot<AF32, TAIL, !AF32>(p.y, e, left) : Slot<AF32>{};
     }
   };
   // One row (t < t1: an idle team only joins the exchange).
-  auto step = [&](int64_t t, const Row& r) {
+  auto step = [&](int t, const Row& r) {
     const bool on = t < t1;
-    float r2 = 0.0f, r1 = 1.0f;
-    if (on) {
-      if (p.da) r2 = p.r_pre[t];
-      if (p.post_norm) r1 = p.r_post[t];
-    }
+    const float r2 = r.r2, r1 = r.r1;
     float sum[3] = {0.0f, 0.0f, 0.0f};
     float xh[VPT][kSlot], dz[VPT][kSlot], yh[VPT][kSlot];
     if (on) {
@@ -240,35 +241,34 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       const int left = d - column(q);
-      const int64_t e = t * d + column(q);
+      const int64_t e = (int64_t)t * d + column(q);
       float out[kSlot];
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
         dz[q][i] = fmaf(-m2, xh[q][i], dz[q][i]);
         out[i] = p.y ? p.alpha * dz[q][i] : dz[q][i];
       }
-      store_slot<RF32, TAIL, true>(p.dx, e, left, pack_slot<RF32>(out));
+      store_slot<RF32, TAIL, !RF32>(p.dx, e, left, pack_slot<RF32>(out));
       if (!p.y) continue;
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
         acc_a[q][i] = fmaf(dz[q][i], yh[q][i], acc_a[q][i]);
         out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
       }
-      store_slot<AF32, TAIL, true>(p.dy, e, left, pack_slot<AF32>(out));
+      store_slot<AF32, TAIL, !AF32>(p.dy, e, left, pack_slot<AF32>(out));
     }
     if constexpr (!MANY) return;
-    const bool ends = (t + 1) % p.gate_every == 0 || t + 1 == p.T;
+    const bool ends = t + 1 == g_end;
     if (!ends && t + 1 != t1) return;
     // the gate's group or the team's rows end here: hand A on
-    const int64_t g = t / p.gate_every;
-    float* out = g * p.gate_every < t0 ? p.part_gate + 2 * b * p.ldp
-                 : !ends               ? p.part_gate + (2 * b + 1) * p.ldp
-                                       : p.dgate + g * d;
+    float* out = (int64_t)g * every < t0 ? p.part_gate + 2 * (int64_t)b * p.ldp
+                 : !ends                 ? p.part_gate + (2 * (int64_t)b + 1) * p.ldp
+                                         : p.dgate + (int64_t)g * d;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
       float wp[kSlot], gt[kSlot];
       load_vec<TAIL>(p.w_post, column(q), d - column(q), wp);
-      load_vec<TAIL>(p.gate, g * d + column(q), d - column(q), gt);
+      load_vec<TAIL>(p.gate, (int64_t)g * d + column(q), d - column(q), gt);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
         const float A = p.beta * acc_a[q][i];
@@ -278,16 +278,21 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
       }
       if (p.dgate) store_slot<true, TAIL>(out, column(q), d - column(q), pack_slot<true>(wp));
     }
-    if (ends && t + 1 < t1) load_c(g + 1);
+    if (ends && t + 1 < t1) {
+      ++g;
+      g_end = min(g_end + every, T);
+      load_c();
+    }
   };
 
+  Row r = {};
+  if (t0 < t1) load_row(t0, r);
 #pragma unroll
   for (int q = 0; q < VPT; ++q) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[q]);
-  if (t0 < p.T) load_c(MANY ? t0 / p.gate_every : 0);
-  for (int64_t t = t0; t < t0 + p.per; ++t) {
-    Row r;
-    if (t < t1) load_row(t, r);
+  if (t0 < T) load_c();
+  for (int t = t0; t < t0 + per; ++t) {
     step(t, r);
+    if (t + 1 < t1) load_row(t + 1, r);
   }
 
   // Column sums over the workgroup's teams, in team order.

@@ -11,6 +11,8 @@
 // partial sums per workgroup, then the scaling, whose workgroups each add the
 // partial sums up again (a launch of its own for that would cost more).
 // Bound by memory: one read for the norm, one read and one write to scale.
+#include <type_traits>
+
 #include "clip.h"
 #include "rows.h"
 
@@ -54,32 +56,62 @@ __device__ __forceinline__ double group_sum_f64(double v, double* lds) {
   return (lds[0] + lds[1]) + (lds[2] + lds[3]);
 }
 
-constexpr int kBatch = 4;  // slots a thread has in flight
+constexpr int kBatch = 4;  // 16-byte loads a thread has in flight
 
-// Calls f(element, elements left, batch of slots) for the chunk's slots of
-// this thread, kBatch at a time; whole slots first, without bounds.
+// Calls f(element, elements, values) for this thread's share of the chunk's n
+// elements from e0: 16-byte pieces (eight bf16 or four fp32 values), kBatch
+// at a time, then the elements that are left one by one.
 template <bool F32, class F>
-__device__ __forceinline__ void for_slots(const void* src, int64_t e0, int n, F f) {
-  constexpr int kStep = 256 * kSlot;
-  int c = threadIdx.x * kSlot;
-  for (; c + (kBatch - 1) * kStep + kSlot <= n; c += kBatch * kStep) {
-    Slot<F32> s[kBatch];
+__device__ __forceinline__ void for_pieces(const void* src, int64_t e0, int n, F f) {
+  constexpr int kPiece = F32 ? 4 : 8, kStep = 256 * kPiece;
+  typedef typename std::conditional<F32, float, bf16_t>::type E;
+  const E* p = static_cast<const E*>(src) + e0;
+  int c = threadIdx.x * kPiece;
+  for (; c + (kBatch - 1) * kStep + kPiece <= n; c += kBatch * kStep) {
+    u32x4 w[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) s[i] = load_slot<F32, false, true>(src, e0 + c + i * kStep, kSlot);
+    for (int i = 0; i < kBatch; ++i) w[i] = get16<true>(p + c + i * kStep);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) f(e0 + c + i * kStep, kSlot, s[i]);
+    for (int i = 0; i < kBatch; ++i) f(c + i * kStep, kPiece, w[i]);
   }
-  for (; c < n; c += kStep) f(e0 + c, n - c, load_slot<F32, true, true>(src, e0 + c, n - c));
+  for (; c < n; c += kStep) {
+    if (c + kPiece <= n) {
+      f(c, kPiece, get16<true>(p + c));
+    } else {
+      for (; c < n; ++c) {
+        uint32_t v;
+        if constexpr (F32)
+          v = __float_as_uint(p[c]);
+        else
+          v = p[c];
+        f(c, 1, u32x4{v, 0, 0, 0});
+      }
+    }
+  }
+}
+
+// The values of a 16-byte piece.
+template <bool F32>
+__device__ __forceinline__ void piece_values(u32x4 w, float (&v)[F32 ? 4 : 8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
 }
 
 template <bool F32>
 __device__ __forceinline__ double chunk_squares(const void* p, int64_t e0, int64_t numel) {
   double s = 0.0;
-  for_slots<F32>(p, e0, (int)min((int64_t)kChunk, numel - e0), [&](int64_t, int, const Slot<F32>& q) {
-    float v[kSlot];
-    unpack_slot<F32>(q, v);
+  for_pieces<F32>(p, e0, (int)min((int64_t)kChunk, numel - e0), [&](int, int, u32x4 w) {
+    float v[F32 ? 4 : 8];
+    piece_values<F32>(w, v);  // zeros behind a single element
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) s = fma((double)v[i], (double)v[i], s);
+    for (float x : v) s = fma((double)x, (double)x, s);
   });
   return s;
 }
@@ -120,12 +152,26 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
 
 template <bool F32>
 __device__ __forceinline__ void scale_chunk(const void* src, void* dst, int64_t e0, int64_t numel, float f) {
-  for_slots<F32>(src, e0, (int)min((int64_t)kChunk, numel - e0), [&](int64_t e, int left, const Slot<F32>& q) {
-    float v[kSlot];
-    unpack_slot<F32>(q, v);
+  typedef typename std::conditional<F32, float, bf16_t>::type E;
+  E* out = static_cast<E*>(dst) + e0;
+  for_pieces<F32>(src, e0, (int)min((int64_t)kChunk, numel - e0), [&](int c, int n, u32x4 w) {
+    float v[F32 ? 4 : 8];
+    piece_values<F32>(w, v);
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) v[i] *= f;
-    store_slot<F32, true, true>(dst, e, left, pack_slot<F32>(v));
+    for (float& x : v) x *= f;
+    if constexpr (F32) {
+      if (n == 4)
+        put16<true>(out + c, u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                   __float_as_uint(v[3])});
+      else
+        out[c] = v[0];
+    } else {
+      if (n == 8)
+        put16<true>(out + c, u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7])});
+      else
+        out[c] = f32_to_bf16(v[0]);
+    }
   });
 }
 
