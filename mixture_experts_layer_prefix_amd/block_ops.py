@@ -3,7 +3,6 @@ sorted by expert and back, the norms before and after a residual block, and
 gradient clipping.  They check their tensors, allocate outputs and workspaces
 with torch and pass pointers and the stream that is current on the tensors'
 device; no arithmetic happens here."""
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -22,12 +21,19 @@ def _act(prec):
     return _ACT[prec]
 
 
+def _address(*args):
+    """_tensors.address, found at the first call."""
+    global _address
+    _address = _lib.tensors().address
+    return _address(*args)
+
+
 def _check(name, t, dtype, shape, device):
     """t as a device pointer; raises unless it is a contiguous tensor of this
     type and shape on this device.  None: a null pointer."""
     if t is None:
         return None
-    p = _lib.tensors().address(t, dtype, shape, device.index)
+    p = _address(t, dtype, shape, device.index)
     if p < 0:
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, not %s of shape %s on %s%s" % (
             name, dtype, shape, device, t.dtype, tuple(t.shape), t.device,
@@ -43,18 +49,16 @@ def _need(name, t):
     return t.device
 
 
-_HERE = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current around a launch (its streams, its kernels)."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _stream(device):
-    """The stream current on `device`, as torch.cuda.current_stream(device)
-    gives it, without making a Stream object (1 us) for each call."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _launch(device, name, *args):
+    """Calls an entry point on the stream that is current on `device`, with
+    that device current.  The stream is what torch.cuda.current_stream(device)
+    gives, read without making a Stream object (1 us) for each call."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            call(name, *args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def _device(device):
@@ -85,23 +89,22 @@ class SortPlan:
         self.x_perm = torch.empty(dims.R, dims.d, dtype=act, device=dev) if x_perm is None and gather else x_perm
         _check("row_token", self.row_token, torch.int32, (dims.R,), dev)
         _check("x_perm", self.x_perm, act, (dims.R, dims.d), dev)
+        self._prec, self._act, self._ids, self._rows = PREC[prec], act, (dims.T, dims.k), (dims.T, dims.d)
         self.ws_bytes = n.value
         self.ws = torch.empty(max(n.value, 16), dtype=torch.uint8, device=dev)
 
     def run(self, topk_idx, x=None):
         """(counts, offsets, row_token, token_row, x_perm) of the ids topk_idx
         [T][k] int32 and the tokens x [T][d]."""
-        D, dev = self.dims, self.device
+        dev = self.device
         if self.x_perm is not None:
             _need("x", x)
         _need("topk_idx", topk_idx)
-        idx = _check("topk_idx", topk_idx, torch.int32, (D.T, D.k), dev)
-        xp = _check("x", x, _ACT[self.prec], (D.T, D.d), dev)
-        with _on(dev):
-            call("moe_sort_tokens", self.cdims, PREC[self.prec], idx, xp, self.counts.data_ptr(),
-                 self.offsets.data_ptr(), self.row_token.data_ptr(), self.token_row.data_ptr(),
-                 None if self.x_perm is None else self.x_perm.data_ptr(), self.ws.data_ptr(), self.ws_bytes,
-                 _stream(dev))
+        idx = _check("topk_idx", topk_idx, torch.int32, self._ids, dev)
+        xp = _check("x", x, self._act, self._rows, dev)
+        _launch(dev, "moe_sort_tokens", self.cdims, self._prec, idx, xp, self.counts.data_ptr(),
+                self.offsets.data_ptr(), self.row_token.data_ptr(), self.token_row.data_ptr(),
+                None if self.x_perm is None else self.x_perm.data_ptr(), self.ws.data_ptr(), self.ws_bytes)
         return self.counts, self.offsets, self.row_token, self.token_row, self.x_perm
 
 
@@ -121,8 +124,7 @@ def sort_tokens_backward(dx_perm, token_row, dx_add, dims: Dims, prec: str, dx=N
     args = (_check("dx_perm", dx_perm, act, (dims.R, dims.d), dev),
             _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
             _check("dx_add", dx_add, act, (dims.T, dims.d), dev), _check("dx", dx, act, (dims.T, dims.d), dev))
-    with _on(dev):
-        call("moe_sort_tokens_backward", dims.c(), PREC[prec], *args, _stream(dev))
+    _launch(dev, "moe_sort_tokens_backward", dims.c(), PREC[prec], *args)
     return dx
 
 
@@ -136,8 +138,7 @@ def unsort_tokens(o_perm, token_row, topk_w, y_add, dims: Dims, prec: str, y=Non
             _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
             _check("topk_w", topk_w, torch.float32, (dims.T, dims.k), dev),
             _check("y_add", y_add, act, (dims.T, dims.d), dev), _check("y", y, act, (dims.T, dims.d), dev))
-    with _on(dev):
-        call("moe_unsort_tokens", dims.c(), PREC[prec], *args, _stream(dev))
+    _launch(dev, "moe_unsort_tokens", dims.c(), PREC[prec], *args)
     return y
 
 
@@ -156,8 +157,7 @@ def unsort_tokens_backward(dy, o_perm, token_row, topk_w, dims: Dims, prec: str,
             _check("token_row", token_row, torch.int32, (dims.T, dims.k), dev),
             _check("topk_w", topk_w, torch.float32, (dims.T, dims.k), dev),
             _check("do_perm", do_perm, act, (dims.R, dims.d), dev), None if dw is None else dw.data_ptr())
-    with _on(dev):
-        call("moe_unsort_tokens_backward", dims.c(), PREC[prec], *args, _stream(dev))
+    _launch(dev, "moe_unsort_tokens_backward", dims.c(), PREC[prec], *args)
     return do_perm, dw
 
 
@@ -198,20 +198,28 @@ class Block:
     def c(self):
         return moe_block(self.T, self.every, self.d, self.res_f32, self.post_norm, self.alpha, self.beta, self.eps)
 
-    def vectors(self, w_pre, w_post, gate, dev):
-        f32 = torch.float32
-        return (_check("w_post", w_post, f32, (self.d,), dev), _check("gate", gate, f32, (self.gates, self.d), dev),
-                _check("w_pre", w_pre, f32, (self.d,), dev))
+
+class _BlockPlan:
+    """What both directions' plans check their tensors against."""
+
+    def __init__(self, block: Block, device):
+        self.block, self.device, self.cblock = block, _device(device), block.c()
+        self._prec, self._act, self._res = PREC[block.prec], block.act, block.res
+        self._rows, self._vec, self._gates = (block.T, block.d), (block.d,), (block.gates, block.d)
+
+    def _vectors(self, w_pre, w_post, gate):
+        f32, dev = torch.float32, self.device
+        return (_check("w_post", w_post, f32, self._vec, dev), _check("gate", gate, f32, self._gates, dev),
+                _check("w_pre", w_pre, f32, self._vec, dev))
 
 
-class BlockNormPlan:
+class BlockNormPlan(_BlockPlan):
     """Outputs of moe_block_norm for one configuration: x_out [T][d] (None
     without a block output), a [T][d] (None with pre_norm=False), r_post and
     r_pre [T] for the backward."""
 
     def __init__(self, block: Block, device="cuda", pre_norm=True):
-        self.block, self.device = block, _device(device)
-        self.cblock = block.c()
+        super().__init__(block, device)
         T, d, dev = block.T, block.d, self.device
         self.x_out = torch.empty(T, d, dtype=block.res, device=dev)
         self.a = torch.empty(T, d, dtype=block.act, device=dev) if pre_norm else None
@@ -220,16 +228,13 @@ class BlockNormPlan:
 
     def run(self, x, y=None, w_pre=None, w_post=None, gate=None):
         """(x_out, a); x_out is x itself where there is no block output y."""
-        b, dev = self.block, self.device
+        dev = self.device
         _need("x", x)
-        px = _check("x", x, b.res, (b.T, b.d), dev)
-        py = _check("y", y, b.act, (b.T, b.d), dev)
-        wp, g, w = b.vectors(w_pre, w_post, gate, dev)
-        with _on(dev):
-            call("moe_block_norm", self.cblock, PREC[b.prec], px, py, wp, g, w,
-                 None if y is None else self.x_out.data_ptr(), None if self.a is None else self.a.data_ptr(),
-                 None if self.r_post is None else self.r_post.data_ptr(),
-                 None if self.r_pre is None else self.r_pre.data_ptr(), _stream(dev))
+        px, py = _check("x", x, self._res, self._rows, dev), _check("y", y, self._act, self._rows, dev)
+        _launch(dev, "moe_block_norm", self.cblock, self._prec, px, py, *self._vectors(w_pre, w_post, gate),
+                None if y is None else self.x_out.data_ptr(), None if self.a is None else self.a.data_ptr(),
+                None if self.r_post is None else self.r_post.data_ptr(),
+                None if self.r_pre is None else self.r_pre.data_ptr())
         return (x if y is None else self.x_out), self.a
 
 
@@ -240,15 +245,14 @@ def block_norm(block: Block, x, y=None, w_pre=None, w_post=None, gate=None, pre_
     return plan.run(x, y, w_pre, w_post, gate) + (plan,)
 
 
-class BlockNormBackwardPlan:
+class BlockNormBackwardPlan(_BlockPlan):
     """Gradients and workspace of moe_block_norm_backward for one
     configuration: dx and dy [T][d], grads of the weights that are given (fp32
     dw_pre, dw_post [d], dgate [gates][d])."""
 
     def __init__(self, block: Block, device="cuda", w_pre=True, w_post=True, gate=False, output=True):
         """output=False: a step without a block output (no dy)."""
-        self.block, self.device = block, _device(device)
-        self.cblock = block.c()
+        super().__init__(block, device)
         T, d, dev = block.T, block.d, self.device
         self.dx = torch.empty(T, d, dtype=block.res, device=dev)
         self.dy = torch.empty(T, d, dtype=block.act, device=dev) if output else None
@@ -265,18 +269,16 @@ class BlockNormBackwardPlan:
     def run(self, dx_out, da, x_out, y, r_pre, r_post, w_pre=None, w_post=None, gate=None):
         """(dx, dy, grads) from the gradients of x_out and a (None: no
         gradient), the forward's x_out, y and row statistics."""
-        b, dev = self.block, self.device
+        dev, rows, tokens, f32 = self.device, self._rows, (self.block.T,), torch.float32
         _need("dx_out or da", da if dx_out is None else dx_out)
-        rows, f32 = (b.T, b.d), torch.float32
-        args = (_check("dx_out", dx_out, b.res, rows, dev), _check("da", da, b.act, rows, dev),
-                _check("x_out", x_out, b.res, rows, dev), _check("y", y, b.act, rows, dev),
-                _check("r_post", r_post, f32, (b.T,), dev), _check("r_pre", r_pre, f32, (b.T,), dev))
-        vec = b.vectors(w_pre, w_post, gate, dev)
+        args = (_check("dx_out", dx_out, self._res, rows, dev), _check("da", da, self._act, rows, dev),
+                _check("x_out", x_out, self._res, rows, dev), _check("y", y, self._act, rows, dev),
+                _check("r_post", r_post, f32, tokens, dev), _check("r_pre", r_pre, f32, tokens, dev))
+        vec = self._vectors(w_pre, w_post, gate)
         g = {n: t.data_ptr() for n, t in self.grads.items()}
-        with _on(dev):
-            call("moe_block_norm_backward", self.cblock, PREC[b.prec], *args, *vec, self.dx.data_ptr(),
-                 None if self.dy is None else self.dy.data_ptr(), g.get("dw_post"), g.get("dgate"), g.get("dw_pre"),
-                 self.ws.data_ptr(), self.ws_bytes, _stream(dev))
+        _launch(dev, "moe_block_norm_backward", self.cblock, self._prec, *args, *vec, self.dx.data_ptr(),
+                None if self.dy is None else self.dy.data_ptr(), g.get("dw_post"), g.get("dgate"), g.get("dw_pre"),
+                self.ws.data_ptr(), self.ws_bytes)
         return self.dx, self.dy, self.grads
 
 
@@ -310,8 +312,7 @@ def grad_norm(grads):
     ptrs, numel, types, dev = _tensors("grads", grads)
     norm = torch.empty(1, dtype=torch.float32, device=dev)
     ws, size = _scratch(numel, len(grads), dev)
-    with _on(dev):
-        call("moe_grad_norm", ptrs, numel, types, len(grads), norm.data_ptr(), ws.data_ptr(), size, _stream(dev))
+    _launch(dev, "moe_grad_norm", ptrs, numel, types, len(grads), norm.data_ptr(), ws.data_ptr(), size)
     return norm
 
 
@@ -334,7 +335,6 @@ def clip_grads(grads, max_norm, norm=None, out=None):
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)
         ws, size = _scratch(numel, len(grads), dev)
-    with _on(dev):
-        call("moe_clip_grads", ptrs, optrs, numel, types, len(grads), max_norm, given, norm.data_ptr(),
-             None if ws is None else ws.data_ptr(), size, _stream(dev))
+    _launch(dev, "moe_clip_grads", ptrs, optrs, numel, types, len(grads), max_norm, given, norm.data_ptr(),
+            None if ws is None else ws.data_ptr(), size)
     return (grads if out is None else out), norm
