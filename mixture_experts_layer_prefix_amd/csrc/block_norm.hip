@@ -172,15 +172,45 @@ struct BwdRow {
 template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   __shared__ float red[2][16][3];
-  __shared__ float cols[1024 * kSlot];
+  // VPT 1: room to add the teams' column sums; VPT 2: the column sums, as
+  // [sum][slot][half][thread], each thread touching its own only
+  __shared__ f32x4 cols[(VPT == 1 ? 1 : 4) * 2 * 1024];
   const int b = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
   const int T = (int)p.T, per = (int)p.per, every = MANY ? (int)p.gate_every : T;
   const int t0 = min(b * per, T), t1 = min(t0 + per, T);
   const int waves = blockDim.x / 64, d = p.d;
   int phase = 0;
   int g = MANY ? t0 / every : 0, g_end = min((g + 1) * every, T);  // the row's gate group and its end
-  float w_pre[VPT][kSlot], c[VPT][kSlot];
-  float acc_pre[VPT][kSlot] = {}, acc_a[VPT][kSlot] = {}, acc_post[VPT][kSlot] = {};  // acc_post: MANY only
+  constexpr bool KEEP = VPT == 1 || !RF32;  // else w_pre is read anew for each row, for want of registers
+  float w_pre[KEEP ? VPT : 1][kSlot], c[VPT][kSlot];
+  constexpr int PRE = 0, A = 1, POST = 2;  // the column sums; POST with MANY only
+  constexpr int NACC = VPT == 1 ? 3 : 1;
+  float acc[NACC][1][kSlot] = {};
+  auto cell = [&](int sum, int q, int half) -> f32x4& { return cols[((sum * VPT + q) * 2 + half) * 1024 + threadIdx.x]; };
+  if constexpr (VPT > 1) {
+#pragma unroll
+    for (int i = 0; i < 4 * VPT; ++i) cell(i / (2 * VPT), i / 2 % VPT, i % 2) = f32x4{};
+  }
+  // Two slots a thread would not leave room for the sums in registers: they
+  // are in LDS then, and the third of them in the team's row of part_post.
+  auto add = [&](int sum, int q, const float (&v)[kSlot]) {
+    if constexpr (VPT == 1) {
+#pragma unroll
+      for (int i = 0; i < kSlot; ++i) acc[sum][0][i] += v[i];
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) cell(sum, q, h) += f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    }
+  };
+  auto value = [&](int sum, int q, float (&v)[kSlot]) {
+#pragma unroll
+    for (int i = 0; i < kSlot; ++i) {
+      if constexpr (VPT == 1)
+        v[i] = acc[sum][0][i];
+      else
+        v[i] = cell(sum, q, i / 4)[i % 4];
+    }
+  };
 
   auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
   auto load_c = [&] {
@@ -193,6 +223,7 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
       for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * gt[i];
     }
   };
+  bool posted = false;
   typedef BwdRow<AF32, RF32, VPT> Row;
   auto load_row = [&](int t, Row& r) {
     r.r2 = p.da ? p.r_pre[t] : 0.0f;
@@ -221,18 +252,20 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
         unpack_slot<AF32>(r.a[q], a);
         unpack_slot<RF32>(r.d[q], dz[q]);
         unpack_slot<AF32>(r.y[q], yh[q]);
+        if constexpr (!KEEP) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[0]);
 #pragma unroll
         for (int i = 0; i < kSlot; ++i) {
           xh[q][i] *= r2;
           yh[q][i] *= r1;
-          acc_pre[q][i] = fmaf(a[i], xh[q][i], acc_pre[q][i]);
-          const float u = a[i] * w_pre[q][i];
+          const float u = a[i] * w_pre[KEEP ? q : 0][i];
           sum[0] = fmaf(u, xh[q][i], sum[0]);
           dz[q][i] = fmaf(r2, u, dz[q][i]);
           const float s = c[q][i] * yh[q][i];
           sum[1] = fmaf(s, dz[q][i], sum[1]);
           sum[2] = fmaf(s, xh[q][i], sum[2]);
+          a[i] *= xh[q][i];
         }
+        add(PRE, q, a);
       }
     }
     team_sum<3>(sum, red, waves, phase);
@@ -251,10 +284,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
       store_slot<RF32, TAIL, !RF32>(p.dx, e, left, pack_slot<RF32>(out));
       if (!p.y) continue;
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) {
-        acc_a[q][i] = fmaf(dz[q][i], yh[q][i], acc_a[q][i]);
-        out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
-      }
+      for (int i = 0; i < kSlot; ++i) out[i] = dz[q][i] * yh[q][i];
+      add(A, q, out);
+#pragma unroll
+      for (int i = 0; i < kSlot; ++i) out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
       store_slot<AF32, TAIL, !AF32>(p.dy, e, left, pack_slot<AF32>(out));
     }
     if constexpr (!MANY) return;
@@ -266,18 +299,35 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
                                          : p.dgate + (int64_t)g * d;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      float wp[kSlot], gt[kSlot];
+      float wp[kSlot], gt[kSlot], sum_a[kSlot];
       load_vec<TAIL>(p.w_post, column(q), d - column(q), wp);
       load_vec<TAIL>(p.gate, (int64_t)g * d + column(q), d - column(q), gt);
+      value(A, q, sum_a);
 #pragma unroll
       for (int i = 0; i < kSlot; ++i) {
-        const float A = p.beta * acc_a[q][i];
-        wp[i] *= A;
-        acc_post[q][i] = fmaf(gt[i], A, acc_post[q][i]);
-        acc_a[q][i] = 0.0f;
+        sum_a[i] *= p.beta;
+        wp[i] *= sum_a[i];
+        gt[i] *= sum_a[i];
       }
       if (p.dgate) store_slot<true, TAIL>(out, column(q), d - column(q), pack_slot<true>(wp));
+      if constexpr (VPT == 1) {
+        add(POST, q, gt);
+#pragma unroll
+        for (int i = 0; i < kSlot; ++i) acc[A][0][i] = 0.0f;
+      } else {
+        cell(A, q, 0) = cell(A, q, 1) = f32x4{};
+        if (p.dw_post) {  // this team's row (one team a workgroup), this thread's columns
+          float* post = p.part_post + blockIdx.x * p.ldp;
+          if (posted) {
+            unpack_slot<true>(load_slot<true, TAIL>(post, column(q), d - column(q)), wp);
+#pragma unroll
+            for (int i = 0; i < kSlot; ++i) gt[i] += wp[i];
+          }
+          store_slot<true, TAIL>(post, column(q), d - column(q), pack_slot<true>(gt));
+        }
+      }
     }
+    posted = true;
     if (ends && t + 1 < t1) {
       ++g;
       g_end = min(g_end + every, T);
@@ -287,8 +337,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
 
   Row r = {};
   if (t0 < t1) load_row(t0, r);
+  if constexpr (KEEP) {
 #pragma unroll
-  for (int q = 0; q < VPT; ++q) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[q]);
+    for (int q = 0; q < VPT; ++q) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[q]);
+  }
   if (t0 < T) load_c();
   for (int t = t0; t < t0 + per; ++t) {
     step(t, r);
@@ -296,31 +348,32 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   }
 
   // Column sums over the workgroup's teams, in team order.
-  auto leave = [&](float (&acc)[VPT][kSlot], float* part) {
+  auto leave = [&](int sum, float* part) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      if (blockDim.y > 1) {
-        float* mine = cols + (threadIdx.y * blockDim.x + threadIdx.x) * kSlot;
+      float v[kSlot];
+      value(sum, q, v);
+      if (VPT == 1 && blockDim.y > 1) {
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kSlot; ++i) mine[i] = acc[q][i];
+        f32x4* mine = cols + (threadIdx.y * blockDim.x + threadIdx.x) * 2;
+        mine[0] = f32x4{v[0], v[1], v[2], v[3]};
+        mine[1] = f32x4{v[4], v[5], v[6], v[7]};
         __syncthreads();
         if (threadIdx.y == 0) {
           for (int k = 1; k < (int)blockDim.y; ++k) {
 #pragma unroll
-            for (int i = 0; i < kSlot; ++i) acc[q][i] += cols[(k * blockDim.x + threadIdx.x) * kSlot + i];
+            for (int i = 0; i < kSlot; ++i) v[i] += cols[(k * blockDim.x + threadIdx.x) * 2 + i / 4][i % 4];
           }
         }
       }
-      if (threadIdx.y == 0)
-        store_slot<true, TAIL>(part + blockIdx.x * p.ldp, column(q), d - column(q), pack_slot<true>(acc[q]));
+      if (threadIdx.y == 0) store_slot<true, TAIL>(part + blockIdx.x * p.ldp, column(q), d - column(q), pack_slot<true>(v));
     }
   };
-  if (p.dw_pre) leave(acc_pre, p.part_pre);
+  if (p.dw_pre) leave(PRE, p.part_pre);
   if constexpr (MANY) {
-    if (p.dw_post) leave(acc_post, p.part_post);
+    if (VPT == 1 && p.dw_post) leave(POST, p.part_post);
   } else if (p.dw_post || p.dgate) {
-    leave(acc_a, p.part_post);
+    leave(A, p.part_post);
   }
 }
 
@@ -398,7 +451,10 @@ void launch_fwd(const BlockNorm& p, hipStream_t s) {
     else
       go(tail ? block_norm_kernel<AF32, RF32, 1, false, true> : block_norm_kernel<AF32, RF32, 1, false, false>);
   } else {
-    go(many ? block_norm_kernel<AF32, RF32, 2, true, true> : block_norm_kernel<AF32, RF32, 2, false, true>);
+    if (many)
+      go(tail ? block_norm_kernel<AF32, RF32, 2, true, true> : block_norm_kernel<AF32, RF32, 2, true, false>);
+    else
+      go(tail ? block_norm_kernel<AF32, RF32, 2, false, true> : block_norm_kernel<AF32, RF32, 2, false, false>);
   }
 }
 
@@ -431,8 +487,10 @@ void launch_bwd(const BlockNormBwd& p, const BwdShape& b, hipStream_t s) {
       go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, false, true>
               : block_norm_bwd_kernel<AF32, RF32, 1, false, false>);
   } else {
-    go(many ? block_norm_bwd_kernel<AF32, RF32, 2, true, true>
-            : block_norm_bwd_kernel<AF32, RF32, 2, false, true>);
+    if (many)
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 2, true, true> : block_norm_bwd_kernel<AF32, RF32, 2, true, false>);
+    else
+      go(tail ? block_norm_bwd_kernel<AF32, RF32, 2, false, true> : block_norm_bwd_kernel<AF32, RF32, 2, false, false>);
   }
 }
 

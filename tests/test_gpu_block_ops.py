@@ -162,7 +162,7 @@ NORMS = [  # T, d, gate_every (0: no gate, -1: one gate row), post, alpha, beta
     (64, 512, -1, False, 0.875, 1.0), (70, 513, 7, True, 1.0, 0.25), (33, 2047, 100, True, 0.5, 1.5),
     (130, 1000, 33, False, 1.0, 1.0), (9, 8193, 4, True, 1.0, 0.5), (4, 16384, -1, True, 0.5, 1.0),
     (1100, 40, 500, True, 0.75, 0.5), (1537, 72, -1, True, 1.0, 1.0), (1030, 16, 1, True, 1.0, 1.0),
-    (1600, 24, 5, False, 1.0, 1.0)]
+    (1600, 24, 5, False, 1.0, 1.0), (300, 9000, 3, True, 0.5, 1.0), (260, 8201, 1, True, 1.0, 2.0)]
 PRECS = [("bf16", False), ("bf16", True), ("f32", False)]
 
 
