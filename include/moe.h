@@ -468,7 +468,7 @@ moe_status moe_block_norm(const moe_block* block, moe_prec prec, const void* x, 
  *   dy = r_post (v - yh mean(v yh))  (post_norm), else dn.
  * Without a block output y and dy are NULL (then x_out is the forward's x).
  * dw_post, dgate, dw_pre (fp32) may be NULL, and need their w_post, gate,
- * w_pre.  An empty batch gives zero dw_post and dw_pre.  Outputs must not
+ * w_pre.  An empty batch gives zero dw_post and dw_pre, and dgate no rows.  Outputs must not
  * overlap inputs.  ws: moe_block_norm_scratch_bytes(T, d) bytes (0 for sizes
  * outside the limits). */
 size_t moe_block_norm_scratch_bytes(int64_t T, int32_t d);

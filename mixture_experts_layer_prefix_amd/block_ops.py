@@ -2,7 +2,9 @@
 sorted by expert and back, the norms before and after a residual block, and
 gradient clipping.  They check their tensors, allocate outputs and workspaces
 with torch and pass pointers and the stream that is current on the tensors'
-device; no arithmetic happens here."""
+device; no arithmetic happens here.  A plan's buffers serve one call at a
+time: calls that may overlap (on two streams, in two graphs replayed at once)
+need plans of their own."""
 import ctypes
 from dataclasses import dataclass
 
@@ -262,7 +264,7 @@ class BlockNormBackwardPlan(_BlockPlan):
         if w_post and block.post_norm:
             self.grads["dw_post"] = torch.empty(d, dtype=torch.float32, device=dev)
         if gate:
-            self.grads["dgate"] = torch.empty(block.gates, d, dtype=torch.float32, device=dev)
+            self.grads["dgate"] = (torch.empty if T else torch.zeros)(block.gates, d, dtype=torch.float32, device=dev)
         self.ws_bytes = _lib.lib().moe_block_norm_scratch_bytes(T, d)
         self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=dev)
 

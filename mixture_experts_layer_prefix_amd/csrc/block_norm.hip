@@ -377,43 +377,22 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   }
 }
 
-// Sums of partial rows, kSumCols columns per workgroup: blockIdx.y 0 is
-// dw_pre; 1 is dw_post and, with one gate row, dgate; 2 + i is the i-th gate
-// group that may span teams.  Eight threads share four columns each, the
-// other 32 ways of the workgroup take the rows in turn; the 32 sums are then
-// added in order.
+// Sums of partial rows, kSumCols columns per workgroup.  Eight threads share
+// four columns each, the other 32 ways of the workgroup take the n rows
+// row(0), row(1), ... of src in turn; the 32 sums are then added in order and
+// given to put(column, sum).
 constexpr int kSumCols = 32;
-__global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int64_t teams, int64_t groups) {
+template <class RowOf, class Put>
+__device__ __forceinline__ void sum_rows(const BlockNormBwd& p, const float* src, int n, RowOf row_of, Put put) {
   __shared__ float lds[32][kSumCols];
-  const int job = blockIdx.y;
-  const bool many = p.gate && p.gate_every < p.T;
-  const float* src = p.part_pre;
-  int64_t n = groups, g = 0, first = 0;
-  if (job == 0 && !p.dw_pre) return;
-  if (job == 1) {
-    src = p.part_post;
-    if (!p.dw_post && (many || !p.dgate)) return;
-  }
-  if (job >= 2) {
-    const int64_t gates = ceil_div(p.T, p.gate_every);
-    g = job - 2;
-    if (gates > teams) g = (min((g + 1) * p.per, p.T) - 1) / p.gate_every;  // the team's last group
-    first = g * p.gate_every / p.per;
-    const int64_t last = (min((g + 1) * p.gate_every, p.T) - 1) / p.per;
-    if (first == last || (gates > teams && first != job - 2)) return;
-    src = p.part_gate;
-    n = last - first + 1;  // row 2 first + 1, then rows 2b for the teams b after it
-  }
   const int col = threadIdx.x & 7, sub = threadIdx.x >> 3;
   const int c = blockIdx.x * kSumCols + col * 4;
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c < p.ldp) {
 #pragma unroll 4
-    for (int64_t i = sub; i < n; i += 32) {
-      const int64_t row = job < 2 ? i : 2 * (first + i) + (i == 0);
-      s += *reinterpret_cast<const f32x4*>(src + row * p.ldp + c);
-    }
+    for (int i = sub; i < n; i += 32) s += *reinterpret_cast<const f32x4*>(src + (int64_t)row_of(i) * p.ldp + c);
   }
+  __syncthreads();  // the sums before have been read
   *reinterpret_cast<f32x4*>(&lds[sub][col * 4]) = s;
   __syncthreads();
   const int out = blockIdx.x * kSumCols + threadIdx.x;
@@ -421,15 +400,37 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int64_t 
   float v = 0.0f;
 #pragma unroll
   for (int i = 0; i < 32; ++i) v += lds[i][threadIdx.x];
-  if (job == 0) {
-    p.dw_pre[out] = v;
-  } else if (job >= 2) {
-    p.dgate[g * p.d + out] = v;
-  } else if (many) {
-    p.dw_post[out] = v;
-  } else {  // v is the column's A
-    if (p.dw_post) p.dw_post[out] = v * (p.gate ? p.beta * p.gate[out] : p.beta);
-    if (p.dgate) p.dgate[out] = v * (p.w_post ? p.beta * p.w_post[out] : p.beta);
+  put(out, v);
+}
+
+// blockIdx.y 0 sums dw_pre; 1 dw_post and, with one gate row, dgate; the rest
+// share the gate groups that span teams: the candidates are the groups or,
+// where those are more than the teams, each team's last group.
+__global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int teams, int groups, int spans) {
+  const bool many = p.gate && p.gate_every < p.T;
+  auto same = [](int i) { return i; };
+  if (blockIdx.y == 0) {
+    if (p.dw_pre) sum_rows(p, p.part_pre, groups, same, [&](int c, float v) { p.dw_pre[c] = v; });
+    return;
+  }
+  if (blockIdx.y == 1) {
+    if (many && p.dw_post) sum_rows(p, p.part_post, groups, same, [&](int c, float v) { p.dw_post[c] = v; });
+    if (!many && (p.dw_post || p.dgate))
+      sum_rows(p, p.part_post, groups, same, [&](int c, float v) {  // v is the column's A
+        if (p.dw_post) p.dw_post[c] = v * (p.gate ? p.beta * p.gate[c] : p.beta);
+        if (p.dgate) p.dgate[c] = v * (p.w_post ? p.beta * p.w_post[c] : p.beta);
+      });
+    return;
+  }
+  const int T = (int)p.T, per = (int)p.per, every = (int)p.gate_every;
+  const bool by_team = (T + every - 1) / every > teams;
+  for (int i = blockIdx.y - 2; i < spans; i += gridDim.y - 2) {
+    const int g = by_team ? (min((i + 1) * per, T) - 1) / every : i;
+    const int first = g * every / per, last = (min((g + 1) * every, T) - 1) / per;
+    if (first == last || (by_team && first != i)) continue;
+    // row 2 first + 1, then rows 2b of the teams b after it
+    sum_rows(p, p.part_gate, last - first + 1, [&](int r) { return 2 * (first + r) + (r == 0); },
+             [&](int c, float v) { p.dgate[(int64_t)g * p.d + c] = v; });
   }
 }
 
@@ -516,6 +517,7 @@ hipError_t launch_block_norm_bwd(bool act_f32, bool res_f32, BlockNormBwd p, voi
   const BwdShape b = bwd_shape(p.T, p.d);
   p.ldp = ceil_div(p.d, kSlot) * kSlot;
   p.per = b.per;
+  if (p.T == 0) p.dgate = nullptr;  // it has no rows
   p.part_pre = static_cast<float*>(scratch);
   p.part_post = p.part_pre + b.groups * p.ldp;
   p.part_gate = p.part_post + b.groups * p.ldp;
@@ -527,10 +529,16 @@ hipError_t launch_block_norm_bwd(bool act_f32, bool res_f32, BlockNormBwd p, voi
     launch_bwd<false, true>(p, b, s);
   else
     launch_bwd<false, false>(p, b, s);
-  const int64_t gates = p.dgate && p.gate_every < p.T ? ceil_div(p.T, p.gate_every) : 0;
-  const unsigned jobs = 2 + (unsigned)(gates < b.teams ? gates : b.teams);
-  if (p.dw_pre || p.dw_post || p.dgate)
-    sum_parts_kernel<<<dim3((unsigned)ceil_div(p.ldp, kSumCols), jobs), 256, 0, s>>>(p, b.teams, b.groups);
+  // teams begin at multiples of per: no group spans two where the gate's period divides it
+  int64_t spans = 0;
+  if (p.dgate && p.gate_every < p.T && p.per % p.gate_every) {
+    spans = ceil_div(p.T, p.gate_every);
+    if (spans > b.teams) spans = b.teams;
+  }
+  if (p.dw_pre || p.dw_post || p.dgate) {
+    const dim3 grid((unsigned)ceil_div(p.ldp, kSumCols), 2 + (unsigned)(spans < 256 ? spans : 256));
+    sum_parts_kernel<<<grid, 256, 0, s>>>(p, (int)b.teams, (int)b.groups, (int)spans);
+  }
   return hipGetLastError();
 }
 
