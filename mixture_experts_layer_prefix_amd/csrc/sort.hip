@@ -202,9 +202,9 @@ __device__ __forceinline__ bool row_here(int64_t row, int64_t R) { return (uint6
 struct RowShape {
   dim3 grid, block;
 };
-RowShape row_shape(int64_t T, int d) {
-  int th = (int)ceil_div(ceil_div(d, kSlot), 64) * 64;  // one slot per thread
-  th = th > 1024 ? 1024 : th;
+RowShape row_shape(int64_t T, int d, int most = 1024) {
+  const int64_t slots = ceil_div(d, kSlot), per = ceil_div(slots, most);  // per thread
+  const int th = (int)ceil_div(ceil_div(slots, per), 64) * 64;
   const int tok = th >= 256 ? 1 : 256 / th;
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
 }
@@ -419,14 +419,15 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
 
 }  // namespace
 
-// Which schedule: kernel times in us, without the 1 to 2 us between launches,
-// for 256 experts and k = 8; "few" holds the copy of the rows, whose own
-// kernel takes 3.0 (d = 512) to 11.3 (d = 7168, 4,096 routes) beside the others.
-//   routes               512   2,048   4,096   32,768   65,536   131,072
-//   few   d = 512/7168   5/6.4 8.8/10.4 13.9/20.8
-//   wide                 4.6   5.0     5.3     9.0      15.1     20
-//   count, scan, rank    8.6   9.8     10.4    13       15       16
-constexpr int64_t kFewRoutes = 2048, kWideLimit = 65536;
+// Which schedule: kernel times in us for 256 experts and k = 8; "few" holds
+// the copy of the rows, whose own kernel takes 3.0 (d = 512) to 11.3 (d = 7168,
+// 4,096 routes) beside the others, and each further launch costs about 1 us.
+//   routes               512    2,048     4,096      32,768  65,536  131,072
+//   few   d = 512/7168   5/6.4  8.8/10.4  13.9/20.8
+//   wide                 4.6    5.0       5.3        9.0     15.1    20
+//   count, scan, rank    8.6    9.8       10.4       13      15      16
+// Whole calls at 65,536 routes (d = 7168): wide 200, count, scan, rank 197.
+constexpr int64_t kFewRoutes = 2048, kWideLimit = 32768;
 
 size_t sort_scratch_bytes(int64_t T, int k, int E) {
   return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
@@ -458,7 +459,7 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
     sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
   }
   if (x_perm) {
-    const RowShape g = row_shape(T, d);
+    const RowShape g = row_shape(T, d, 512);  // 8,192 x 7,168, k = 8: 183 us; with up to 1,024 threads 187
     ROW_KERNEL(sort_rows_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
   }
   return hipGetLastError();
