@@ -11,11 +11,28 @@
 //   unsort backward  do_perm[row_j] = w_j dy[t], dw_j = <dy[t], o_perm[row_j]>
 // with j over the present routes in slot order, fp32 sums and one rounding.
 // Every one of them is a single pass over the rows, bound by memory.
+#include <type_traits>
+
 #include "rows.h"
 
 namespace moe {
 
 namespace {
+
+// Elements of a 16-byte slot: the lanes of a wave then read and write whole
+// cache lines with one instruction, as streaming wants them.
+template <bool F32>
+constexpr int kPer = F32 ? 4 : 8;
+template <bool F32>
+using Slot16 = Slot<F32, kPer<F32>>;
+template <bool F32, bool TAIL, bool STREAM = false>
+__device__ __forceinline__ Slot16<F32> load16(const void* p, int64_t e, int left) {
+  return load_slot<F32, TAIL, STREAM, kPer<F32>>(p, e, left);
+}
+template <bool F32, bool TAIL, bool STREAM = false>
+__device__ __forceinline__ void store16(void* p, int64_t e, int left, const Slot16<F32>& s) {
+  store_slot<F32, TAIL, STREAM, kPer<F32>>(p, e, left, s);
+}
 
 constexpr int kSortRoutes = 256;  // routes per schedule workgroup, one per thread
 
@@ -202,8 +219,8 @@ __device__ __forceinline__ bool row_here(int64_t row, int64_t R) { return (uint6
 struct RowShape {
   dim3 grid, block;
 };
-RowShape row_shape(int64_t T, int d, int most = 1024) {
-  const int64_t slots = ceil_div(d, kSlot), per = ceil_div(slots, most);  // per thread
+RowShape row_shape(bool f32, int64_t T, int d, int most = 1024) {
+  const int64_t slots = ceil_div(d, f32 ? 4 : 8), per = ceil_div(slots, most);  // per thread
   const int th = (int)ceil_div(ceil_div(slots, per), 64) * 64;
   const int tok = th >= 256 ? 1 : 256 / th;
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
@@ -251,9 +268,9 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
     return;
   }
   const int r0 = t * k;
-  int c = threadIdx.x * kSlot;  // the token's first slots are under way while the rows are found
-  Slot<F32> s = {};
-  if (xp) s = load_slot<F32, TAIL>(x, (int64_t)t * d + c, d - c);
+  int c = threadIdx.x * kPer<F32>;  // the token's first slots are under way while the rows are found
+  Slot16<F32> s = {};
+  if (xp) s = load16<F32, TAIL>(x, (int64_t)t * d + c, d - c);
   int before[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) before[j] = 0;
@@ -289,33 +306,35 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
   while (c < d) {
     for (int j = 0; j < k; ++j) {
       const int row = __builtin_amdgcn_readfirstlane(h[j]);
-      if (row >= 0) store_slot<F32, TAIL>(xp, (int64_t)row * d + c, d - c, s);
+      if (row >= 0) store16<F32, TAIL>(xp, (int64_t)row * d + c, d - c, s);
     }
-    c += blockDim.x * kSlot;
-    if (c < d) s = load_slot<F32, TAIL>(x, (int64_t)t * d + c, d - c);
+    c += blockDim.x * kPer<F32>;
+    if (c < d) s = load16<F32, TAIL>(x, (int64_t)t * d + c, d - c);
   }
 }
 
 constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
 
-template <bool F32, bool TAIL>
+// STREAM: writes with the hint that they are not read again soon.
+template <bool F32, bool TAIL, bool STREAM>
 __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
                                                          const int32_t* __restrict__ token_row, void* __restrict__ xp,
                                                          int64_t T, int k, int d) {
   const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;
-  for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
-    const Slot<F32> s = load_slot<F32, TAIL>(x, t * d + c, d - c);
+  for (int c = threadIdx.x * kPer<F32>; c < d; c += blockDim.x * kPer<F32>) {
+    const Slot16<F32> s = load16<F32, TAIL>(x, t * d + c, d - c);
     for (int j = 0; j < k; ++j) {
       const int64_t row = token_row[t * k + j];
-      if (row_here(row, T * k)) store_slot<F32, TAIL>(xp, row * d + c, d - c, s);
+      if (row_here(row, T * k)) store16<F32, TAIL, STREAM>(xp, row * d + c, d - c, s);
     }
   }
 }
 
 // y[t] = sum_j w_j rows[row_j] + add[t]; w NULL: every weight 1, add NULL: 0.
 // add may be y: a slot is read before the thread that read it writes it.
-template <bool F32, bool TAIL>
+// STREAM: reads with the hint that they are not read again.
+template <bool F32, bool TAIL, bool STREAM>
 __global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ rows,
                                                       const int32_t* __restrict__ token_row,
                                                       const float* __restrict__ w, const void* add, void* y, int64_t T,
@@ -323,34 +342,34 @@ __global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ r
   const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;
   const int32_t* tr = token_row + t * k;
-  for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
-    float acc[kSlot] = {}, v[kSlot];
-    Slot<F32> a;
-    if (add) a = load_slot<F32, TAIL>(add, t * d + c, d - c);
+  for (int c = threadIdx.x * kPer<F32>; c < d; c += blockDim.x * kPer<F32>) {
+    float acc[kPer<F32>] = {}, v[kPer<F32>];
+    Slot16<F32> a;
+    if (add) a = load16<F32, TAIL, STREAM>(add, t * d + c, d - c);
     for (int j0 = 0; j0 < k; j0 += kRoutes) {
-      Slot<F32> s[kRoutes];
+      Slot16<F32> s[kRoutes];
       bool here[kRoutes];
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
         const int64_t row = j0 + j < k ? tr[j0 + j] : -1;
         here[j] = row_here(row, T * k);
-        if (here[j]) s[j] = load_slot<F32, TAIL>(rows, row * d + c, d - c);
+        if (here[j]) s[j] = load16<F32, TAIL, STREAM>(rows, row * d + c, d - c);
       }
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
         if (!here[j]) continue;
         const float g = w ? w[t * k + j0 + j] : 1.0f;
-        unpack_slot<F32>(s[j], v);
+        unpack_slot(s[j], v);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+        for (int i = 0; i < kPer<F32>; ++i) acc[i] = fmaf(g, v[i], acc[i]);
       }
     }
     if (add) {
-      unpack_slot<F32>(a, v);
+      unpack_slot(a, v);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) acc[i] += v[i];
+      for (int i = 0; i < kPer<F32>; ++i) acc[i] += v[i];
     }
-    store_slot<F32, TAIL>(y, t * d + c, d - c, pack_slot<F32>(acc));
+    store16<F32, TAIL, true>(y, t * d + c, d - c, pack_slot<F32>(acc));
   }
 }
 
@@ -369,30 +388,30 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
   const int64_t R = T * k;
   for (int j0 = 0; j0 < k; j0 += kRoutes) {
     float dot[kRoutes] = {};
-    for (int c = threadIdx.x * kSlot; c < d; c += blockDim.x * kSlot) {
-      float a[kSlot], b[kSlot];
-      const Slot<F32> q = load_slot<F32, TAIL>(dy, t * d + c, d - c);
-      Slot<F32> s[kRoutes];
+    for (int c = threadIdx.x * kPer<F32>; c < d; c += blockDim.x * kPer<F32>) {
+      float a[kPer<F32>], b[kPer<F32>];
+      const Slot16<F32> q = load16<F32, TAIL>(dy, t * d + c, d - c);
+      Slot16<F32> s[kRoutes];
       int64_t row[kRoutes];
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
         row[j] = j0 + j < k ? tr[j0 + j] : -1;
-        if (dw && row_here(row[j], R)) s[j] = load_slot<F32, TAIL, true>(o, row[j] * d + c, d - c);
+        if (dw && row_here(row[j], R)) s[j] = load16<F32, TAIL, true>(o, row[j] * d + c, d - c);
       }
-      unpack_slot<F32>(q, a);
+      unpack_slot(q, a);
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
         if (!row_here(row[j], R)) continue;
         if (dw) {
-          unpack_slot<F32>(s[j], b);
+          unpack_slot(s[j], b);
 #pragma unroll
-          for (int i = 0; i < kSlot; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
+          for (int i = 0; i < kPer<F32>; ++i) dot[j] = fmaf(a[i], b[i], dot[j]);
         }
         if (dov) {
           const float g = w[t * k + j0 + j];
 #pragma unroll
-          for (int i = 0; i < kSlot; ++i) b[i] = g * a[i];
-          store_slot<F32, TAIL>(dov, row[j] * d + c, d - c, pack_slot<F32>(b));
+          for (int i = 0; i < kPer<F32>; ++i) b[i] = g * a[i];
+          store16<F32, TAIL, true>(dov, row[j] * d + c, d - c, pack_slot<F32>(b));
         }
       }
     }
@@ -413,9 +432,25 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
   }
 }
 
-// A kernel's instance for an element type and a row length.
-#define ROW_KERNEL(name, f32, d)                                                  \
-  ((d) % kSlot ? ((f32) ? name<true, true> : name<false, true>) : ((f32) ? name<true, false> : name<false, false>))
+// Rows that the last cache level (256 MB) holds little of are read and written
+// with the streaming hint; smaller ones are likely to be in it, having just
+// been written, or to be read from it next.
+bool beyond_caches(bool f32, int64_t rows, int d) { return rows * d * (f32 ? 4 : 2) > (384ll << 20); }
+
+// The instance of a kernel for an element type, a row length and a hint:
+// pick(F32, TAIL, STREAM) with std::bool_constant arguments.
+template <class Pick>
+auto row_kernel(bool f32, int d, bool stream, Pick pick) {
+  constexpr std::true_type yes;
+  constexpr std::false_type no;
+  const bool tail = d % (f32 ? 4 : 8) != 0;
+  if (f32) {
+    if (stream) return tail ? pick(yes, yes, yes) : pick(yes, no, yes);
+    return tail ? pick(yes, yes, no) : pick(yes, no, no);
+  }
+  if (stream) return tail ? pick(no, yes, yes) : pick(no, no, yes);
+  return tail ? pick(no, yes, no) : pick(no, no, no);
+}
 
 }  // namespace
 
@@ -442,10 +477,12 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
   }
   const int64_t R = T * k;
   if (R <= kFewRoutes) {
-    const int slots = (int)ceil_div(d, kSlot);
+    const int slots = (int)ceil_div(d, f32 ? 4 : 8);
     const int th = slots <= 256 ? 256 : slots >= 1024 ? 1024 : (slots + 63) / 64 * 64;
-    ROW_KERNEL(sort_few_kernel, f32, d)
-    <<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm);
+    const auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
+      return sort_few_kernel<F32.value, TAIL.value>;
+    });
+    kernel<<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm);
     return hipGetLastError();
   }
   if (R <= kWideLimit) {
@@ -459,8 +496,15 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
     sort_rank_kernel<<<nb, kSortRoutes, 0, s>>>(topk_idx, R, E, k, bc, counts, offsets, row_token, token_row);
   }
   if (x_perm) {
-    const RowShape g = row_shape(T, d, 512);  // 8,192 x 7,168, k = 8: 183 us; with up to 1,024 threads 187
-    ROW_KERNEL(sort_rows_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
+    const RowShape g = row_shape(f32, T, d, 512);  // 8,192 x 7,168, k = 8: 183 us; with up to 1,024 threads 187
+    // Streaming writes want whole cache lines.  65,536 bf16 rows of 7,168: 197
+    // us a call, streaming 170; of 4,096: 134, 116; of 3,000 (no whole lines):
+    // 108, 121; of 2,048 (within the cache): 58, 63.
+    const bool stream = beyond_caches(f32, R, d) && d % (f32 ? 32 : 64) == 0;
+    const auto kernel = row_kernel(f32, d, stream, [](auto F32, auto TAIL, auto STREAM) {
+      return sort_rows_kernel<F32.value, TAIL.value, STREAM.value>;
+    });
+    kernel<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
   }
   return hipGetLastError();
 }
@@ -468,17 +512,24 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
 hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, const float* w, const void* add, void* y,
                          int64_t T, int d, int k, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const RowShape g = row_shape(T, d);
-  ROW_KERNEL(unsort_kernel, f32, d)<<<g.grid, g.block, 0, s>>>(rows, token_row, w, add, y, T, k, d);
+  const RowShape g = row_shape(f32, T, d);
+  // 65,536 bf16 rows of 7,168: 215 us, streaming 196; of 4,096: 121, 109; of
+  // 1,536: 37.7, 41.3.  The sums are streamed in any case: 226 us without.
+  const auto kernel = row_kernel(f32, d, beyond_caches(f32, T * k, d), [](auto F32, auto TAIL, auto STREAM) {
+    return unsort_kernel<F32.value, TAIL.value, STREAM.value>;
+  });
+  kernel<<<g.grid, g.block, 0, s>>>(rows, token_row, w, add, y, T, k, d);
   return hipGetLastError();
 }
 
 hipError_t launch_unsort_bwd(bool f32, const void* dy, const void* o_perm, const int32_t* token_row, const float* w,
                              void* do_perm, float* dw, int64_t T, int d, int k, hipStream_t s) {
   if (T == 0) return hipSuccess;
-  const RowShape g = row_shape(T, d);
-  ROW_KERNEL(unsort_bwd_kernel, f32, d)
-  <<<g.grid, g.block, 0, s>>>(dy, o_perm, token_row, w, do_perm, dw, T, k, d);
+  const RowShape g = row_shape(f32, T, d);
+  const auto kernel = row_kernel(f32, d, true, [](auto F32, auto TAIL, auto) {
+    return unsort_bwd_kernel<F32.value, TAIL.value>;
+  });
+  kernel<<<g.grid, g.block, 0, s>>>(dy, o_perm, token_row, w, do_perm, dw, T, k, d);
   return hipGetLastError();
 }
 
