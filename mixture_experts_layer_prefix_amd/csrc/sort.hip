@@ -315,8 +315,7 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
 
 constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
 
-// STREAM: writes with the hint that they are not read again soon.
-template <bool F32, bool TAIL, bool STREAM>
+template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
                                                          const int32_t* __restrict__ token_row, void* __restrict__ xp,
                                                          int64_t T, int k, int d) {
@@ -326,7 +325,7 @@ __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict_
     const Slot16<F32> s = load16<F32, TAIL>(x, t * d + c, d - c);
     for (int j = 0; j < k; ++j) {
       const int64_t row = token_row[t * k + j];
-      if (row_here(row, T * k)) store16<F32, TAIL, STREAM>(xp, row * d + c, d - c, s);
+      if (row_here(row, T * k)) store16<F32, TAIL>(xp, row * d + c, d - c, s);
     }
   }
 }
@@ -497,12 +496,10 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
   }
   if (x_perm) {
     const RowShape g = row_shape(f32, T, d, 512);  // 8,192 x 7,168, k = 8: 183 us; with up to 1,024 threads 187
-    // Streaming writes want whole cache lines.  65,536 bf16 rows of 7,168: 197
-    // us a call, streaming 170; of 4,096: 134, 116; of 3,000 (no whole lines):
-    // 108, 121; of 2,048 (within the cache): 58, 63.
-    const bool stream = beyond_caches(f32, R, d) && d % (f32 ? 32 : 64) == 0;
-    const auto kernel = row_kernel(f32, d, stream, [](auto F32, auto TAIL, auto STREAM) {
-      return sort_rows_kernel<F32.value, TAIL.value, STREAM.value>;
+    // Streaming the writes gains nothing here (8,192 x 7,168, k = 8: 196 to 197
+    // us either way) and costs up to 10% where the rows fit the last cache level.
+    const auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
+      return sort_rows_kernel<F32.value, TAIL.value>;
     });
     kernel<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
   }
