@@ -16,17 +16,24 @@
 // so one exchange per row carries all three sums.
 //
 // fp32 throughout; outputs are rounded once.  Both directions read and write
-// every row once and are bound by memory.  bf16 outputs are written with the
-// streaming hint (8,192 x 7,168 forward: 98 us without, 78 with), and the
-// backward also reads with it (16,384 x 7,168: 298, 286); fp32 slots, two
-// 16-byte accesses a lane, are not: each fills only half of the lines it
-// touches (fp32 backward, 8,192 x 7,168: 321 us with, 291 without).
+// every row once and are bound by memory.  A slot is 16 bytes of the residual,
+// so that one instruction of a wave covers whole cache lines: fp32 in slots of
+// 32 bytes, each access filling half of its lines, took 106 us for 8,192 x
+// 4,096 forward, in 16 bytes 83.  The forward's outputs are written with the
+// streaming hint (8,192 x 7,168 bf16: 98 us without, 78 with).
+#include <type_traits>
+
 #include "block_norm.h"
 #include "rows.h"
 
 namespace moe {
 
 namespace {
+
+// Channels of a thread's slot: 16 bytes of bf16, or of fp32 where the residual
+// is fp32 (the activations' slots are then 8 bytes where they are bf16).
+template <bool RF32>
+constexpr int kPer = RF32 ? 4 : 8;
 
 // Sums of NV values over the `waves` waves of a team in wave order, for all
 // teams of the workgroup at once; exchanges alternate between the halves of
@@ -54,13 +61,13 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], float (*lds)[16][NV], i
 __device__ __forceinline__ float rms_inverse(float sum, int d, float eps) { return 1.0f / sqrtf(sum / d + eps); }
 
 // A slot of an fp32 vector, ones where the vector is missing.
-template <bool TAIL>
-__device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, float (&out)[kSlot]) {
+template <bool TAIL, int N>
+__device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, float (&out)[N]) {
   if (v) {
-    unpack_slot<true>(load_slot<true, TAIL>(v, e, left), out);
+    unpack_slot(load_slot<true, TAIL, false, N>(v, e, left), out);
   } else {
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) out[i] = 1.0f;
+    for (int i = 0; i < N; ++i) out[i] = 1.0f;
   }
 }
 
@@ -72,39 +79,40 @@ __device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, fl
 // read anew for every row they would be 12 bytes a channel from L2 beside the
 // row's 8 bytes from memory.  TAIL: d is not a multiple of the slot.
 template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
-__global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(BlockNorm p) {
+__global__ void __launch_bounds__(1024, VPT * kPer<RF32> <= 8 ? 8 : 4) block_norm_kernel(BlockNorm p) {
+  constexpr int N = kPer<RF32>;
   __shared__ float lds[2][16][1];
   const int waves = blockDim.x / 64, d = p.d;
   const int64_t teams = (int64_t)gridDim.x * blockDim.y;
   int phase = 0;
-  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
-  float w_pre[VPT][kSlot], c[VPT][kSlot];
+  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * N; };
+  float w_pre[VPT][N], c[VPT][N];
 #pragma unroll
   for (int q = 0; q < VPT; ++q) {
     const int e = column(q), left = d - e;
-    float v[kSlot];
+    float v[N];
     load_vec<TAIL>(p.w_pre, e, left, w_pre[q]);
     load_vec<TAIL>(p.w_post, e, left, c[q]);
     load_vec<TAIL>(MANY ? nullptr : p.gate, e, left, v);
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * v[i];
+    for (int i = 0; i < N; ++i) c[q][i] *= p.beta * v[i];
   }
   const int64_t first = (int64_t)blockIdx.x * blockDim.y;
   for (int64_t t0 = first; t0 < p.T; t0 += teams) {
     const int64_t t = uniform_i64(t0 + threadIdx.y);
     const bool on = t < p.T;
-    float z[VPT][kSlot], v[kSlot], sum[1] = {0.0f}, r = 1.0f;
-    Slot<RF32> xs[VPT];
+    float z[VPT][N], v[N], sum[1] = {0.0f}, r = 1.0f;
+    Slot<RF32, N> xs[VPT];
     if (on) {
 #pragma unroll
       for (int q = 0; q < VPT; ++q) {
         const int left = d - column(q);
         const int64_t e = t * d + column(q);
-        xs[q] = load_slot<RF32, TAIL>(p.x, e, left);
+        xs[q] = load_slot<RF32, TAIL, false, N>(p.x, e, left);
         if (p.y) {
-          unpack_slot<AF32>(load_slot<AF32, TAIL>(p.y, e, left), z[q]);
+          unpack_slot(load_slot<AF32, TAIL, false, N>(p.y, e, left), z[q]);
 #pragma unroll
-          for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
+          for (int i = 0; i < N; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
         }
       }
     }
@@ -124,17 +132,17 @@ __global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(Bloc
           if constexpr (MANY) {
             load_vec<TAIL>(p.gate, g * d + column(q), left, v);
 #pragma unroll
-            for (int i = 0; i < kSlot; ++i) z[q][i] *= v[i];
+            for (int i = 0; i < N; ++i) z[q][i] *= v[i];
           }
-          unpack_slot<RF32>(xs[q], v);
+          unpack_slot(xs[q], v);
 #pragma unroll
-          for (int i = 0; i < kSlot; ++i) z[q][i] = fmaf(p.alpha, v[i], c[q][i] * (z[q][i] * r));
-          store_slot<RF32, TAIL, !RF32>(p.x_out, e, left, pack_slot<RF32>(z[q]));
+          for (int i = 0; i < N; ++i) z[q][i] = fmaf(p.alpha, v[i], c[q][i] * (z[q][i] * r));
+          store_slot<RF32, TAIL, true, N>(p.x_out, e, left, pack_slot<RF32>(z[q]));
         } else {
-          unpack_slot<RF32>(xs[q], z[q]);
+          unpack_slot(xs[q], z[q]);
         }
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
+        for (int i = 0; i < N; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
       }
     }
     if (!p.a) continue;
@@ -145,8 +153,8 @@ __global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(Bloc
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) z[q][i] *= r * w_pre[q][i];
-      store_slot<AF32, TAIL, !AF32>(p.a, t * d + column(q), d - column(q), pack_slot<AF32>(z[q]));
+      for (int i = 0; i < N; ++i) z[q][i] *= r * w_pre[q][i];
+      store_slot<AF32, TAIL, true, N>(p.a, t * d + column(q), d - column(q), pack_slot<AF32>(z[q]));
     }
   }
 }
@@ -154,9 +162,10 @@ __global__ void __launch_bounds__(1024, VPT == 1 ? 8 : 4) block_norm_kernel(Bloc
 // The raw slots of one row: x', da, dx', y; and its r_pre and r_post.
 template <bool AF32, bool RF32, int VPT>
 struct BwdRow {
+  static constexpr int N = kPer<RF32>;
   float r2, r1;
-  Slot<RF32> x[VPT], d[VPT];
-  Slot<AF32> a[VPT], y[VPT];
+  Slot<RF32, N> x[VPT], d[VPT];
+  Slot<AF32, N> a[VPT], y[VPT];
 };
 
 // Workgroups of up to 16 waves, one per compute unit; a workgroup holds
@@ -172,59 +181,60 @@ struct BwdRow {
 // and one that begins here and goes on to row 2b + 1.  The teams' column sums
 // are added over the workgroup and left as its row of part_pre and part_post
 // (A where there is one gate row); sum_parts_kernel adds those rows.
-// MANY: several gate rows.  TAIL: d is not a multiple of the slot.
-template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
+// MANY: several gate rows.  TAIL: d is not a multiple of the slot.  STREAM:
+// rows are read and written with the streaming hint.
+template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL, bool STREAM>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
+  constexpr int N = kPer<RF32>, Q = N / 4;
+  // Up to eight channels a thread the column sums are in registers, and cols
+  // is room to add the teams' sums; for sixteen they are in LDS, as
+  // [sum][slot][quarter][thread], each thread touching its own only.
+  constexpr bool REG = VPT * N <= 8;
   __shared__ float red[2][16][3];
-  // VPT 1: room to add the teams' column sums; VPT 2: the column sums, as
-  // [sum][slot][half][thread], each thread touching its own only
-  __shared__ f32x4 cols[(VPT == 1 ? 1 : 4) * 2 * 1024];
+  __shared__ f32x4 cols[(REG ? 1 : 2 * VPT) * Q * 1024];
   const int b = __builtin_amdgcn_readfirstlane(blockIdx.x * blockDim.y + threadIdx.y);
   const int T = (int)p.T, per = (int)p.per, every = MANY ? (int)p.gate_every : T;
   const int t0 = min(b * per, T), t1 = min(t0 + per, T);
   const int waves = blockDim.x / 64, d = p.d;
   int phase = 0;
   int g = MANY ? t0 / every : 0, g_end = min((g + 1) * every, T);  // the row's gate group and its end
-  constexpr bool KEEP = VPT == 1 || !RF32;  // else w_pre is read anew for each row, for want of registers
-  float w_pre[KEEP ? VPT : 1][kSlot], c[VPT][kSlot];
+  constexpr bool KEEP = REG || !RF32;  // else w_pre is read anew for each row, for want of registers
+  float w_pre[KEEP ? VPT : 1][N], c[VPT][N];
   constexpr int PRE = 0, A = 1, POST = 2;  // the column sums; POST with MANY only
-  constexpr int NACC = VPT == 1 ? 3 : 1;
-  float acc[NACC][1][kSlot] = {};
-  auto cell = [&](int sum, int q, int half) -> f32x4& { return cols[((sum * VPT + q) * 2 + half) * 1024 + threadIdx.x]; };
-  if constexpr (VPT > 1) {
+  float acc[REG ? 3 : 1][REG ? VPT : 1][N] = {};
+  auto cell = [&](int sum, int q, int h) -> f32x4& { return cols[((sum * VPT + q) * Q + h) * 1024 + threadIdx.x]; };
+  if constexpr (!REG) {  // the third sum is in the team's row of part_post
 #pragma unroll
-    for (int i = 0; i < 4 * VPT; ++i) cell(i / (2 * VPT), i / 2 % VPT, i % 2) = f32x4{};
+    for (int i = 0; i < 2 * VPT * Q; ++i) cell(i / (VPT * Q), i / Q % VPT, i % Q) = f32x4{};
   }
-  // Two slots a thread would not leave room for the sums in registers: they
-  // are in LDS then, and the third of them in the team's row of part_post.
-  auto add = [&](int sum, int q, const float (&v)[kSlot]) {
-    if constexpr (VPT == 1) {
+  auto add = [&](int sum, int q, const float (&v)[N]) {
+    if constexpr (REG) {
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) acc[sum][0][i] += v[i];
+      for (int i = 0; i < N; ++i) acc[sum][q][i] += v[i];
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) cell(sum, q, h) += f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+      for (int h = 0; h < Q; ++h) cell(sum, q, h) += f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
     }
   };
-  auto value = [&](int sum, int q, float (&v)[kSlot]) {
+  auto value = [&](int sum, int q, float (&v)[N]) {
 #pragma unroll
-    for (int i = 0; i < kSlot; ++i) {
-      if constexpr (VPT == 1)
-        v[i] = acc[sum][0][i];
+    for (int i = 0; i < N; ++i) {
+      if constexpr (REG)
+        v[i] = acc[sum][q][i];
       else
         v[i] = cell(sum, q, i / 4)[i % 4];
     }
   };
 
-  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * kSlot; };
+  auto column = [&](int q) { return (q * (int)blockDim.x + (int)threadIdx.x) * N; };
   auto load_c = [&] {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      float gt[kSlot];
+      float gt[N];
       load_vec<TAIL>(p.w_post, column(q), d - column(q), c[q]);
       load_vec<TAIL>(p.gate, (int64_t)g * d + column(q), d - column(q), gt);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) c[q][i] *= p.beta * gt[i];
+      for (int i = 0; i < N; ++i) c[q][i] *= p.beta * gt[i];
     }
   };
   bool posted = false;
@@ -236,10 +246,10 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
     for (int q = 0; q < VPT; ++q) {
       const int left = d - column(q);
       const int64_t e = (int64_t)t * d + column(q);
-      r.x[q] = p.da ? load_slot<RF32, TAIL, !RF32>(p.x_out, e, left) : Slot<RF32>{};
-      r.a[q] = p.da ? load_slot<AF32, TAIL, !AF32>(p.da, e, left) : Slot<AF32>{};
-      r.d[q] = p.dx_out ? load_slot<RF32, TAIL, !RF32>(p.dx_out, e, left) : Slot<RF32>{};
-      r.y[q] = p.y ? load_slot<AF32, TAIL, !AF32>(p.y, e, left) : Slot<AF32>{};
+      r.x[q] = p.da ? load_slot<RF32, TAIL, STREAM, N>(p.x_out, e, left) : Slot<RF32, N>{};
+      r.a[q] = p.da ? load_slot<AF32, TAIL, STREAM, N>(p.da, e, left) : Slot<AF32, N>{};
+      r.d[q] = p.dx_out ? load_slot<RF32, TAIL, STREAM, N>(p.dx_out, e, left) : Slot<RF32, N>{};
+      r.y[q] = p.y ? load_slot<AF32, TAIL, STREAM, N>(p.y, e, left) : Slot<AF32, N>{};
     }
   };
   // One row (t < t1: an idle team only joins the exchange).
@@ -247,18 +257,18 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
     const bool on = t < t1;
     const float r2 = r.r2, r1 = r.r1;
     float sum[3] = {0.0f, 0.0f, 0.0f};
-    float xh[VPT][kSlot], dz[VPT][kSlot], yh[VPT][kSlot];
+    float xh[VPT][N], dz[VPT][N], yh[VPT][N];
     if (on) {
 #pragma unroll
       for (int q = 0; q < VPT; ++q) {
-        float a[kSlot];
-        unpack_slot<RF32>(r.x[q], xh[q]);
-        unpack_slot<AF32>(r.a[q], a);
-        unpack_slot<RF32>(r.d[q], dz[q]);
-        unpack_slot<AF32>(r.y[q], yh[q]);
+        float a[N];
+        unpack_slot(r.x[q], xh[q]);
+        unpack_slot(r.a[q], a);
+        unpack_slot(r.d[q], dz[q]);
+        unpack_slot(r.y[q], yh[q]);
         if constexpr (!KEEP) load_vec<TAIL>(p.w_pre, column(q), d - column(q), w_pre[0]);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) {
+        for (int i = 0; i < N; ++i) {
           xh[q][i] *= r2;
           yh[q][i] *= r1;
           const float u = a[i] * w_pre[KEEP ? q : 0][i];
@@ -279,20 +289,20 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
     for (int q = 0; q < VPT; ++q) {
       const int left = d - column(q);
       const int64_t e = (int64_t)t * d + column(q);
-      float out[kSlot];
+      float out[N];
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) {
+      for (int i = 0; i < N; ++i) {
         dz[q][i] = fmaf(-m2, xh[q][i], dz[q][i]);
         out[i] = p.y ? p.alpha * dz[q][i] : dz[q][i];
       }
-      store_slot<RF32, TAIL, !RF32>(p.dx, e, left, pack_slot<RF32>(out));
+      store_slot<RF32, TAIL, STREAM, N>(p.dx, e, left, pack_slot<RF32>(out));
       if (!p.y) continue;
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) out[i] = dz[q][i] * yh[q][i];
+      for (int i = 0; i < N; ++i) out[i] = dz[q][i] * yh[q][i];
       add(A, q, out);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
-      store_slot<AF32, TAIL, !AF32>(p.dy, e, left, pack_slot<AF32>(out));
+      for (int i = 0; i < N; ++i) out[i] = r1 * fmaf(c[q][i], dz[q][i], -m1 * yh[q][i]);
+      store_slot<AF32, TAIL, STREAM, N>(p.dy, e, left, pack_slot<AF32>(out));
     }
     if constexpr (!MANY) return;
     const bool ends = t + 1 == g_end;
@@ -303,31 +313,32 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
                                          : p.dgate + (int64_t)g * d;
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      float wp[kSlot], gt[kSlot], sum_a[kSlot];
+      float wp[N], gt[N], sum_a[N];
       load_vec<TAIL>(p.w_post, column(q), d - column(q), wp);
       load_vec<TAIL>(p.gate, (int64_t)g * d + column(q), d - column(q), gt);
       value(A, q, sum_a);
 #pragma unroll
-      for (int i = 0; i < kSlot; ++i) {
+      for (int i = 0; i < N; ++i) {
         sum_a[i] *= p.beta;
         wp[i] *= sum_a[i];
         gt[i] *= sum_a[i];
       }
-      if (p.dgate) store_slot<true, TAIL>(out, column(q), d - column(q), pack_slot<true>(wp));
-      if constexpr (VPT == 1) {
+      if (p.dgate) store_slot<true, TAIL, false, N>(out, column(q), d - column(q), pack_slot<true>(wp));
+      if constexpr (REG) {
         add(POST, q, gt);
 #pragma unroll
-        for (int i = 0; i < kSlot; ++i) acc[A][0][i] = 0.0f;
+        for (int i = 0; i < N; ++i) acc[A][q][i] = 0.0f;
       } else {
-        cell(A, q, 0) = cell(A, q, 1) = f32x4{};
+#pragma unroll
+        for (int h = 0; h < Q; ++h) cell(A, q, h) = f32x4{};
         if (p.dw_post) {  // this team's row (one team a workgroup), this thread's columns
           float* post = p.part_post + blockIdx.x * p.ldp;
           if (posted) {
-            unpack_slot<true>(load_slot<true, TAIL>(post, column(q), d - column(q)), wp);
+            unpack_slot(load_slot<true, TAIL, false, N>(post, column(q), d - column(q)), wp);
 #pragma unroll
-            for (int i = 0; i < kSlot; ++i) gt[i] += wp[i];
+            for (int i = 0; i < N; ++i) gt[i] += wp[i];
           }
-          store_slot<true, TAIL>(post, column(q), d - column(q), pack_slot<true>(gt));
+          store_slot<true, TAIL, false, N>(post, column(q), d - column(q), pack_slot<true>(gt));
         }
       }
     }
@@ -355,27 +366,27 @@ __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   auto leave = [&](int sum, float* part) {
 #pragma unroll
     for (int q = 0; q < VPT; ++q) {
-      float v[kSlot];
+      float v[N];
       value(sum, q, v);
-      if (VPT == 1 && blockDim.y > 1) {
+      if (REG && blockDim.y > 1) {
         __syncthreads();
-        f32x4* mine = cols + (threadIdx.y * blockDim.x + threadIdx.x) * 2;
-        mine[0] = f32x4{v[0], v[1], v[2], v[3]};
-        mine[1] = f32x4{v[4], v[5], v[6], v[7]};
+        f32x4* mine = cols + (threadIdx.y * blockDim.x + threadIdx.x) * Q;
+#pragma unroll
+        for (int h = 0; h < Q; ++h) mine[h] = f32x4{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
         __syncthreads();
         if (threadIdx.y == 0) {
           for (int k = 1; k < (int)blockDim.y; ++k) {
 #pragma unroll
-            for (int i = 0; i < kSlot; ++i) v[i] += cols[(k * blockDim.x + threadIdx.x) * 2 + i / 4][i % 4];
+            for (int i = 0; i < N; ++i) v[i] += cols[(k * blockDim.x + threadIdx.x) * Q + i / 4][i % 4];
           }
         }
       }
-      if (threadIdx.y == 0) store_slot<true, TAIL>(part + blockIdx.x * p.ldp, column(q), d - column(q), pack_slot<true>(v));
+      if (threadIdx.y == 0) store_slot<true, TAIL, false, N>(part + blockIdx.x * p.ldp, column(q), d - column(q), pack_slot<true>(v));
     }
   };
   if (p.dw_pre) leave(PRE, p.part_pre);
   if constexpr (MANY) {
-    if (VPT == 1 && p.dw_post) leave(POST, p.part_post);
+    if (REG && p.dw_post) leave(POST, p.part_post);
   } else if (p.dw_post || p.dgate) {
     leave(A, p.part_post);
   }
@@ -438,72 +449,87 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(BlockNormBwd p, int team
   }
 }
 
-// Threads per row (whole waves) for VPT slots each.
-int team_threads(int d, int vpt) { return (int)ceil_div(ceil_div(d, kSlot * vpt), 64) * 64; }
+// A row's threads (whole waves), for rows of up to 16,384 channels at most
+// 1,024 with as few slots each as that takes; and the rows of a workgroup.
+struct TeamShape {
+  int vpt, th, tpb;
+};
+TeamShape team_shape(int d, bool res_f32) {
+  const int per = res_f32 ? 4 : 8;
+  TeamShape s;
+  s.vpt = 1;
+  while (d > 1024 * per * s.vpt) s.vpt *= 2;
+  s.th = (int)ceil_div(ceil_div(d, per * s.vpt), 64) * 64;
+  s.tpb = 1024 / s.th;
+  return s;
+}
+
+// Calls f with VPT, MANY and TAIL as std::integral_constant values.
+template <bool RF32, class F>
+void with_shape(int vpt, bool many, bool tail, F f) {
+  auto flags = [&](auto v) {
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    if (many)
+      tail ? f(v, yes, yes) : f(v, yes, no);
+    else
+      tail ? f(v, no, yes) : f(v, no, no);
+  };
+  if (vpt == 1) return flags(std::integral_constant<int, 1>());
+  if (vpt == 2) return flags(std::integral_constant<int, 2>());
+  if constexpr (RF32) flags(std::integral_constant<int, 4>());
+}
 
 template <bool AF32, bool RF32>
 void launch_fwd(const BlockNorm& p, hipStream_t s) {
   constexpr int64_t kGroups = 512;  // two workgroups of 16 waves per compute unit
-  const int vpt = p.d <= 1024 * kSlot ? 1 : 2, th = team_threads(p.d, vpt), tpb = 1024 / th;
-  const int64_t groups = ceil_div(p.T, tpb);
-  auto go = [&](auto kernel) {
-    kernel<<<dim3((unsigned)(groups < kGroups ? groups : kGroups)), dim3(th, tpb), 0, s>>>(p);
-  };
-  const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
-  if (vpt == 1) {
-    if (many)
-      go(tail ? block_norm_kernel<AF32, RF32, 1, true, true> : block_norm_kernel<AF32, RF32, 1, true, false>);
-    else
-      go(tail ? block_norm_kernel<AF32, RF32, 1, false, true> : block_norm_kernel<AF32, RF32, 1, false, false>);
-  } else {
-    if (many)
-      go(tail ? block_norm_kernel<AF32, RF32, 2, true, true> : block_norm_kernel<AF32, RF32, 2, true, false>);
-    else
-      go(tail ? block_norm_kernel<AF32, RF32, 2, false, true> : block_norm_kernel<AF32, RF32, 2, false, false>);
-  }
+  const TeamShape t = team_shape(p.d, RF32);
+  const int64_t groups = ceil_div(p.T, t.tpb);
+  with_shape<RF32>(t.vpt, p.gate && p.gate_every < p.T, p.d % kPer<RF32> != 0, [&](auto V, auto MANY, auto TAIL) {
+    block_norm_kernel<AF32, RF32, V.value, MANY.value, TAIL.value>
+        <<<dim3((unsigned)(groups < kGroups ? groups : kGroups)), dim3(t.th, t.tpb), 0, s>>>(p);
+  });
 }
 
 // The backward's workgroups: up to 16 waves, one workgroup per compute unit.
 struct BwdShape {
-  int vpt, th, tpb;      // slots per thread, threads per team, teams per workgroup
-  int64_t per, teams, groups;
+  TeamShape t;
+  int64_t per, teams, groups;  // rows of a team, teams, workgroups
 };
-BwdShape bwd_shape(int64_t T, int d) {
+BwdShape bwd_shape(int64_t T, int d, bool res_f32) {
   constexpr int64_t kGroups = 256;
   BwdShape s;
-  s.vpt = d <= 1024 * kSlot ? 1 : 2;
-  s.th = team_threads(d, s.vpt);
-  s.tpb = 1024 / s.th;
-  s.per = T ? ceil_div(T, kGroups * s.tpb) : 1;
+  s.t = team_shape(d, res_f32);
+  s.per = T ? ceil_div(T, kGroups * s.t.tpb) : 1;
   s.teams = ceil_div(T, s.per);
-  s.groups = ceil_div(s.teams, s.tpb);
+  s.groups = ceil_div(s.teams, s.t.tpb);
   return s;
 }
 
 template <bool AF32, bool RF32>
 void launch_bwd(const BlockNormBwd& p, const BwdShape& b, hipStream_t s) {
-  auto go = [&](auto kernel) { kernel<<<dim3((unsigned)b.groups), dim3(b.th, b.tpb), 0, s>>>(p); };
-  const bool many = p.gate && p.gate_every < p.T, tail = p.d % kSlot != 0;
-  if (b.vpt == 1) {
-    if (many)
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, true, true>
-              : block_norm_bwd_kernel<AF32, RF32, 1, true, false>);
+  with_shape<RF32>(b.t.vpt, p.gate && p.gate_every < p.T, p.d % kPer<RF32> != 0, [&](auto V, auto MANY, auto TAIL) {
+    // Rows that the last cache level (256 MB) cannot hold stream, where they
+    // are whole slots: 16,384 x 7,168 bf16 286 us, else 298; 8,192 x 4,096 with
+    // an fp32 residual 127, else 131; 1,531 x 2,047 (56 MB) 27.6, else 23.4.
+    auto go = [&](auto kernel) { kernel<<<dim3((unsigned)b.groups), dim3(b.t.th, b.t.tpb), 0, s>>>(p); };
+    if (!TAIL.value && p.T * p.d * 3 * ((AF32 ? 4 : 2) + (RF32 ? 4 : 2)) > (256ll << 20))
+      go(block_norm_bwd_kernel<AF32, RF32, V.value, MANY.value, false, true>);
     else
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 1, false, true>
-              : block_norm_bwd_kernel<AF32, RF32, 1, false, false>);
-  } else {
-    if (many)
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 2, true, true> : block_norm_bwd_kernel<AF32, RF32, 2, true, false>);
-    else
-      go(tail ? block_norm_bwd_kernel<AF32, RF32, 2, false, true> : block_norm_bwd_kernel<AF32, RF32, 2, false, false>);
-  }
+      go(block_norm_bwd_kernel<AF32, RF32, V.value, MANY.value, TAIL.value, false>);
+  });
 }
 
 }  // namespace
 
 size_t block_norm_scratch_bytes(int64_t T, int d) {
-  const BwdShape b = bwd_shape(T, d);
-  return (size_t)(2 * b.groups + 2 * b.teams) * (size_t)(ceil_div(d, kSlot) * kSlot) * sizeof(float);
+  size_t rows = 0;
+  for (bool res_f32 : {false, true}) {  // either residual type
+    const BwdShape b = bwd_shape(T, d, res_f32);
+    const size_t n = (size_t)(2 * b.groups + 2 * b.teams);
+    rows = n > rows ? n : rows;
+  }
+  return rows * (size_t)(ceil_div(d, 8) * 8) * sizeof(float);
 }
 
 hipError_t launch_block_norm(bool act_f32, bool res_f32, const BlockNorm& p, hipStream_t s) {
@@ -518,8 +544,8 @@ hipError_t launch_block_norm(bool act_f32, bool res_f32, const BlockNorm& p, hip
 }
 
 hipError_t launch_block_norm_bwd(bool act_f32, bool res_f32, BlockNormBwd p, void* scratch, hipStream_t s) {
-  const BwdShape b = bwd_shape(p.T, p.d);
-  p.ldp = ceil_div(p.d, kSlot) * kSlot;
+  const BwdShape b = bwd_shape(p.T, p.d, act_f32 || res_f32);
+  p.ldp = ceil_div(p.d, 8) * 8;
   p.per = b.per;
   if (p.T == 0) p.dgate = nullptr;  // it has no rows
   p.part_pre = static_cast<float*>(scratch);
