@@ -11,6 +11,8 @@
 // partial sums per workgroup, then the scaling, whose workgroups each add the
 // partial sums up again (a launch of its own for that would cost more).
 // Bound by memory: one read for the norm, one read and one write to scale.
+// 604 MB of bf16 into other buffers: 100 + 193 us (6.0 and 6.3 TB/s); 600
+// tensors of odd sizes, 205 MB, eight launches: 125 us.
 #include <type_traits>
 
 #include "clip.h"

@@ -10,7 +10,13 @@
 //   unsort           y[t] = sum_j w_j o_perm[row_j] (+ y_add[t])
 //   unsort backward  do_perm[row_j] = w_j dy[t], dw_j = <dy[t], o_perm[row_j]>
 // with j over the present routes in slot order, fp32 sums and one rounding.
-// Every one of them is a single pass over the rows, bound by memory.
+// Every one of them is a single pass over the rows, bound by memory: a
+// workgroup takes a token (several where one wave is enough for the row), a
+// thread a 16-byte slot of it, and the token's row numbers are scalars.  On
+// new inputs, bf16: sort of 8,192 x 7,168 with k = 8, an eighth of the tokens
+// absent, 197 us (4.8 TB/s, 14 us of it the schedule); unsort of 16,384 x
+// 6,144 with one route in eight present 98 us (6.2 TB/s); unsort backward of
+// 8,192 x 4,096 with k = 8 209 us (5.5 TB/s).  A copy reaches 5.0 TB/s.
 #include <type_traits>
 
 #include "rows.h"
@@ -36,7 +42,9 @@ __device__ __forceinline__ void store16(void* p, int64_t e, int left, const Slot
 
 constexpr int kSortRoutes = 256;  // routes per schedule workgroup, one per thread
 
-// Routes per expert of each workgroup's 256 routes, expert-major.
+// The schedule in three launches, for any number of routes (65,536: 15 us):
+// routes per expert of each workgroup's 256 routes, expert-major; prefixes per
+// expert; the rows.
 __global__ void __launch_bounds__(kSortRoutes) sort_count_kernel(const int32_t* __restrict__ idx, int64_t R, int E,
                                                                  int32_t* __restrict__ block_counts) {
   __shared__ int32_t h[1024];
@@ -330,6 +338,8 @@ __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict_
   }
 }
 
+// The rows of up to eight present routes are in flight before the first is
+// added (one after another: 166 us where this takes 101).
 // y[t] = sum_j w_j rows[row_j] + add[t]; w NULL: every weight 1, add NULL: 0.
 // add may be y: a slot is read before the thread that read it writes it.
 // STREAM: reads with the hint that they are not read again.
@@ -372,6 +382,8 @@ __global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ r
   }
 }
 
+// dy's slot is read once for all routes, o's rows stream through and so do the
+// gradient's (8,192 x 4,096, k = 8: 232 us without the hint on the writes, 209).
 // Weights (dov) and rows of o (dw) are read only for the output they serve.
 template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ o,

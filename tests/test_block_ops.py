@@ -208,3 +208,21 @@ def test_reference_sort_gradients_match_differences():
         e[row, 1] = h
         diff = ((B.unsort_ref(o + e, token_row, w, None)[0] - B.unsort_ref(o - e, token_row, w, None)[0]) * dy).sum()
         assert abs(diff / (2 * h) - do[row][1]) < 1e-9
+
+
+# ---- the wrappers' helper module --------------------------------------------
+def test_tensor_helper_module():
+    import numpy as np
+    h = L.tensors()
+    t = torch.zeros(2, 3)
+    assert h.address(t, torch.float32, (2, 3), 0) == -1  # not on a GPU
+    assert h.address(3, torch.float32, (2, 3), 0) == -1
+    assert h.describe([]) == (b"", b"", b"", -1)
+    assert h.describe([t]) == 0 and h.describe([None, t]) == 0
+    with pytest.raises(TypeError):
+        h.address(t, torch.float32, [2, 3], 0)
+    with pytest.raises(TypeError):
+        h.distinct(b"", "")
+    pack = lambda v, n: (np.array(v, np.uint64).tobytes(), np.array(n, np.int64).tobytes())  # noqa: E731
+    assert h.distinct(*pack([16, 32], [1, 1])) and h.distinct(*pack([16, 16], [1, 0]))
+    assert not h.distinct(*pack([16, 32, 16], [1, 1, 2]))

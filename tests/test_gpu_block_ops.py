@@ -344,6 +344,51 @@ def test_clip_of_a_tensor_of_more_than_2_30_elements():
     assert bool((t == 0.125).all())
 
 
+# ---- more than 2^31 elements -----------------------------------------------
+def test_routed_rows_of_more_than_2_31_elements():
+    g = gen(9)
+    T, d, E, k = 50000, 7168, 16, 8  # 40,000 x 8 rows of 7,168 are present
+    dims = M.Dims(T, d, E, k, 1)
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.to(torch.int32)
+    idx[::5] = -1
+    x = randn(g, (T, d), torch.bfloat16)
+    _, offsets, row_token, token_row, x_perm = M.sort_tokens(idx, x, dims, "bf16")
+    n = int(offsets[-1])
+    assert n * d > 2 ** 31
+    for a in range(0, n, 50000):
+        b = min(a + 50000, n)
+        assert torch.equal(x_perm[a:b], x[row_token[a:b].long()])
+    here = torch.ones(T, 1, device="cuda", dtype=torch.bfloat16)
+    here[::5] = 0
+    ones = torch.ones(T, k, device="cuda")
+    assert torch.equal(M.unsort_tokens(x_perm, token_row, ones, None, dims, "bf16"), x * 8 * here)  # exact
+    assert torch.equal(M.sort_tokens_backward(x_perm, token_row, None, dims, "bf16"), x * 8 * here)
+    do, dw = M.unsort_tokens_backward(x, x_perm, token_row, ones * 0.5, dims, "bf16")
+    for a in range(0, n, 50000):
+        b = min(a + 50000, n)
+        assert torch.equal(do[a:b], x_perm[a:b] * 0.5)
+    assert bool((dw[::5] == 0).all()) and torch.equal(dw[1], dw[1, :1].expand(k))
+
+
+def test_block_norm_of_more_than_2_31_elements():
+    """Rows far into the tensors give what the same rows give alone."""
+    g = gen(10)
+    n, d, copies = 1000, 7168, 310
+    small = M.Block(n, d, post_norm=True, alpha=0.5)
+    big = M.Block(n * copies, d, post_norm=True, alpha=0.5)
+    assert big.T * d > 2 ** 31
+    p = [randn(g, (n, d), torch.bfloat16) for _ in range(4)]
+    w = [randn(g, (d,)) for _ in range(2)] + [randn(g, (1, d))]
+    P = [t.repeat(copies, 1) for t in p]
+    x1, a1, plan1 = M.block_norm(small, p[0], p[1], *w)
+    X1, A1, plan2 = M.block_norm(big, P[0], P[1], *w)
+    same = lambda big, small: bool((big.view(copies, *small.shape) == small).all())  # noqa: E731
+    assert same(X1, x1) and same(A1, a1) and same(plan2.r_pre, plan1.r_pre) and same(plan2.r_post, plan1.r_post)
+    dx, dy, _ = M.block_norm_backward(small, p[2], p[3], x1, p[1], plan1.r_pre, plan1.r_post, *w)
+    DX, DY, _ = M.block_norm_backward(big, P[2], P[3], X1, P[1], plan2.r_pre, plan2.r_post, *w)
+    assert same(DX, dx) and same(DY, dy)
+
+
 # ---- streams, graphs, repeats ----------------------------------------------
 def step_inputs():
     T, d, E, k = 600, 200, 12, 4
