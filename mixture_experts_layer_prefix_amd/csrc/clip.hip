@@ -190,6 +190,7 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double* _
   const EntryIndex<ClipTable> index(t);
   for (uint32_t c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
     const int i = index.find(c);
+    if (f == 1.0f && t.src[i] == t.dst[i]) continue;  // in place and nothing to clip: the bits are there
     const int64_t e0 = (int64_t)(c - t.first[i]) * kChunk;
     const uint32_t m = t.numel[i];
     if (m & kF32Entry)
