@@ -386,10 +386,10 @@ moe_status moe_bf16_mma_tiles(const void* a, const void* b, const float* c, floa
  * the gradients of both: a route whose expert id lies outside [0, E) is
  * absent (a padding token, a dropped route, an expert of another rank, whose
  * ids become local by subtracting the rank's first expert).  Of `dims` only
- * T, d, k and, in moe_sort_tokens, E are read: T <= 4,194,303, any d >= 1,
- * 1 <= k <= 16 (k may exceed E), E <= 1024.  MOE_F32 and MOE_BF16; rows need
- * element alignment only.  Indices are int32.  Outputs must not overlap
- * inputs, except that y may be y_add and dx may be dx_add.
+ * T, d, k and, in moe_sort_tokens, E are read: T <= 4,194,303,
+ * 1 <= d <= 2^30, 1 <= k <= 16 (k may exceed E), E <= 1024.  MOE_F32 and
+ * MOE_BF16; rows need element alignment only.  Indices are int32.  Outputs
+ * must not overlap inputs, except that y may be y_add and dx may be dx_add.
  *
  * moe_sort_tokens: the present routes in (token, slot) order, grouped by
  * expert (blog post, "Choosing the right communication direction /

@@ -13,6 +13,8 @@ namespace {
 // Workgroups times threads of a launch stay below 2^32.
 constexpr int64_t kMaxTokens = 4194303;
 constexpr int kMaxNormDim = 16384;
+// The row kernels count columns in an int, in steps of at most 8,192.
+constexpr int kMaxRowDim = 1 << 30;
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool need(const void* p, size_t n) { return p && aligned_to(p, n); }
@@ -28,7 +30,7 @@ moe_status check_prec(moe_prec prec) {
 moe_status check_routes(const moe_dims* D, moe_prec prec, bool experts) {
   if (!D || D->T < 0 || D->d < 1 || D->k < 1 || D->k > 16) return MOE_EINVAL;
   if (experts && (D->E < 1 || D->E > 1024)) return MOE_EINVAL;
-  if (D->T > kMaxTokens) return MOE_EUNSUPPORTED;
+  if (D->T > kMaxTokens || D->d > kMaxRowDim) return MOE_EUNSUPPORTED;
   return check_prec(prec);
 }
 
