@@ -550,7 +550,7 @@ hipError_t launch_block_norm_bwd(bool act_f32, bool res_f32, BlockNormBwd p, voi
   const BwdShape b = bwd_shape(p.T, p.d, act_f32 || res_f32);
   p.ldp = ceil_div(p.d, 8) * 8;
   p.per = b.per;
-  if (p.T == 0) p.dgate = nullptr;  // it has no rows
+  if (p.T == 0) p.gate = p.w_post = p.dgate = nullptr;  // the gate has no rows, and zero sums need no factor
   p.part_pre = static_cast<float*>(scratch);
   p.part_post = p.part_pre + b.groups * p.ldp;
   p.part_gate = p.part_post + b.groups * p.ldp;
