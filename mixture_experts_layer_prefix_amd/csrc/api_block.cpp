@@ -120,8 +120,8 @@ moe_status moe_unsort_tokens_backward(const moe_dims* dims, moe_prec prec, const
                                       const int32_t* token_row, const float* topk_w, void* do_perm, float* dtopk_w,
                                       void* stream) {
   MOE_TRY(check_routes(dims, prec, false));
+  if (dims->T == 0) return MOE_OK;  // empty tensors may have no address
   if (!do_perm && !dtopk_w) return MOE_EINVAL;
-  if (dims->T == 0) return MOE_OK;
   const size_t n = elem(prec);
   if (!need(dy, n) || !need(token_row, 4)) return MOE_EINVAL;
   if (do_perm && (!aligned_to(do_perm, n) || !need(topk_w, 4) || do_perm == o_perm || do_perm == dy))

@@ -26,3 +26,13 @@ def test_wide_rows_are_refused(d, prec):
 def test_the_widest_row_has_a_workspace():
     n = ctypes.c_size_t(0)
     assert L.lib().moe_workspace_bytes(M.Dims(1, 1 << 30, 8, 1, 1).c(), BF, 5, ctypes.byref(n)) == L.MOE_OK
+
+
+# ---- empty batches ---------------------------------------------------------
+def test_empty_batches_need_no_addresses():
+    """torch gives tensors without elements the null address."""
+    lib, e = L.lib(), M.Dims(0, 100, 8, 2, 1).c()
+    assert lib.moe_unsort_tokens_backward(e, BF, None, None, None, None, None, None, None) == L.MOE_OK
+    assert lib.moe_unsort_tokens_backward(M.Dims(1, 100, 8, 2, 1).c(), BF, A, A, A, A, None, None, None) == L.MOE_EINVAL
+    b = M.Block(0, 100).c()
+    assert lib.moe_block_norm(b, BF, *[None] * 9, None) == L.MOE_OK

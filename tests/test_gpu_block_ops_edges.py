@@ -25,3 +25,13 @@ def test_empty_batch_has_zero_weight_gradients(prec, res_f32, every):
     assert dx.shape == dy.shape == (0, 24) and set(grads) == {"dw_pre", "dw_post", "dgate"}
     for name, t in grads.items():
         assert bool((t == 0).all()), name
+
+
+@pytest.mark.parametrize("need_do,need_dw", [(True, True), (True, False), (False, True)])
+def test_empty_batch_of_the_weighted_sums_gradient(need_do, need_dw):
+    dims = M.Dims(0, 24, 6, 2, 1)
+    x, w = torch.empty(0, 24, device="cuda"), torch.empty(0, 2, device="cuda")
+    do, dw = M.unsort_tokens_backward(x, x, torch.empty(0, 2, dtype=torch.int32, device="cuda"), w, dims, "f32",
+                                      need_do=need_do, need_dw=need_dw)
+    assert (do.shape == (0, 24)) if need_do else do is None
+    assert (dw.shape == (0, 2)) if need_dw else dw is None
