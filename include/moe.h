@@ -494,8 +494,9 @@ moe_status moe_grad_norm(const void* const* grads, const int64_t* numel, const i
 /* out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), fp32 product rounded
  * once; out (HOST array of device pointers) may hold the tensors of grads
  * themselves (in place) or others of the same types; no tensor of out may
- * otherwise overlap another of either list.  norm_in (device, fp32): the norm
- * to clip by, for instance one joined over ranks; norm and ws are then unused.
+ * otherwise overlap another of either list, nor norm_in.  norm_in (device,
+ * fp32): the norm to clip by, for instance one joined over ranks; norm and ws
+ * are then unused.
  * norm_in NULL: the norm of these tensors, left in *norm, the same bits as
  * moe_grad_norm's.  A NaN norm gives NaN, an infinite one zeros (NaN where a
  * gradient is not finite).  max_norm: finite, >= 0.

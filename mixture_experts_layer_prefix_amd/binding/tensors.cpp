@@ -9,8 +9,12 @@
 //     objects of uint64, int64 and int32 (1 bf16, 0 fp32) and the GPU's index
 //     (-1: no tensors); an int, the index of the first other tensor, instead
 //     where there is one.
-//   distinct(addresses, counts) -> bool: whether no two of describe's tensors
-//     of at least one element share an address.
+//   distinct(addresses, counts[, types, sources, norm]) -> bool: whether the
+//     outputs (describe's addresses, counts and types; without types one byte
+//     an element) can be written in any order while the sources (addresses of
+//     as many tensors of the same counts and types) and the fp32 value at norm
+//     (0: none) are read: no two outputs overlap, and no output overlaps norm
+//     or a source other than its own, which it may only be itself.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -84,18 +88,48 @@ PyObject* describe(PyObject*, PyObject* list) {
 }
 
 PyObject* distinct(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 2 || !PyBytes_Check(a[0]) || !PyBytes_Check(a[1]) || PyBytes_GET_SIZE(a[0]) != PyBytes_GET_SIZE(a[1])) {
-    PyErr_SetString(PyExc_TypeError, "distinct(addresses, counts)");
+  const bool lists = n == 2 || n == 5;
+  for (Py_ssize_t i = 0; lists && i < std::min<Py_ssize_t>(n, 4); ++i)
+    if (!PyBytes_Check(a[i]) || PyBytes_GET_SIZE(a[i]) != PyBytes_GET_SIZE(a[0]) / (i == 2 ? 2 : 1)) n = 0;
+  if (!lists || n == 0) {
+    PyErr_SetString(PyExc_TypeError, "distinct(addresses, counts[, types, sources, norm])");
     return nullptr;
   }
+  const auto* out = reinterpret_cast<const uint64_t*>(PyBytes_AS_STRING(a[0]));
+  const auto* count = reinterpret_cast<const int64_t*>(PyBytes_AS_STRING(a[1]));
+  const auto* type = n == 5 ? reinterpret_cast<const int32_t*>(PyBytes_AS_STRING(a[2])) : nullptr;
+  const auto* src = n == 5 ? reinterpret_cast<const uint64_t*>(PyBytes_AS_STRING(a[3])) : nullptr;
+  const uint64_t norm = n == 5 ? PyLong_AsUnsignedLongLong(a[4]) : 0;
+  if (PyErr_Occurred()) return nullptr;
   try {
-    const auto* p = reinterpret_cast<const uint64_t*>(PyBytes_AS_STRING(a[0]));
-    const auto* m = reinterpret_cast<const int64_t*>(PyBytes_AS_STRING(a[1]));
-    std::vector<uint64_t> v;
-    for (Py_ssize_t i = 0; i < PyBytes_GET_SIZE(a[0]) / 8; ++i)
-      if (m[i] > 0) v.push_back(p[i]);
-    std::sort(v.begin(), v.end());
-    return PyBool_FromLong(std::adjacent_find(v.begin(), v.end()) == v.end());
+    struct Range {
+      uint64_t begin, end;
+      Py_ssize_t i;
+    };
+    const Py_ssize_t m = PyBytes_GET_SIZE(a[0]) / 8;
+    auto bytes = [&](Py_ssize_t i) { return (uint64_t)count[i] * (type ? (type[i] ? 2 : 4) : 1); };
+    std::vector<Range> v;
+    v.reserve(m);
+    for (Py_ssize_t i = 0; i < m; ++i)
+      if (count[i] > 0) v.push_back({out[i], out[i] + bytes(i), i});
+    std::sort(v.begin(), v.end(), [](const Range& p, const Range& q) { return p.begin < q.begin; });
+    for (size_t i = 1; i < v.size(); ++i)
+      if (v[i].begin < v[i - 1].end) Py_RETURN_FALSE;
+    // The output that [begin, end) overlaps: the last one to begin before end,
+    // if any (outputs do not overlap, so that an earlier one ends where the
+    // last one begins at the latest).
+    auto hit = [&](uint64_t begin, uint64_t end) -> const Range* {
+      const auto p = std::lower_bound(v.begin(), v.end(), end, [](const Range& r, uint64_t e) { return r.begin < e; });
+      return p == v.begin() || p[-1].end <= begin ? nullptr : &p[-1];
+    };
+    if (norm && hit(norm, norm + 4)) Py_RETURN_FALSE;
+    if (src && !std::equal(src, src + m, out)) {
+      for (Py_ssize_t i = 0; i < m; ++i) {
+        const Range* r = count[i] > 0 ? hit(src[i], src[i] + bytes(i)) : nullptr;
+        if (r && (r->i != i || r->begin != src[i])) Py_RETURN_FALSE;
+      }
+    }
+    Py_RETURN_TRUE;
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
     return nullptr;

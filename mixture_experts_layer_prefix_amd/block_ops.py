@@ -322,17 +322,18 @@ def clip_grads(grads, max_norm, norm=None, out=None):
     """moe_clip_grads: scales the gradients to a global norm of at most
     max_norm, in place or into the tensors `out`; returns (out, norm).  norm
     (fp32 [1]): the norm to clip by, for instance one joined over ranks; None:
-    that of these tensors."""
+    that of these tensors.  A tensor that is written may overlap no other one
+    of either list and not norm."""
     ptrs, numel, types, dev = _tensors("grads", grads)
     optrs = ptrs
     if out is not None:
         optrs, onumel, otypes, odev = _tensors("out", out)
         if onumel != numel or otypes != types or odev != dev:
             raise ValueError("out must match grads in number, size, type and device")
-    if not _lib.tensors().distinct(optrs, numel):
-        raise ValueError("a tensor would be scaled twice: %s holds one more than once" % ("grads" if out is None
-                                                                                         else "out"))
     given = _check("norm", norm, torch.float32, (1,), dev)
+    if not _lib.tensors().distinct(optrs, numel, types, ptrs, given or 0):
+        raise ValueError("%s overlap each other%s or norm" % (("grads", "") if out is None else
+                                                              ("tensors of out", ", another's gradient")))
     ws, size = None, 0
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=dev)

@@ -36,3 +36,62 @@ def test_empty_batches_need_no_addresses():
     assert lib.moe_unsort_tokens_backward(M.Dims(1, 100, 8, 2, 1).c(), BF, A, A, A, A, None, None, None) == L.MOE_EINVAL
     b = M.Block(0, 100).c()
     assert lib.moe_block_norm(b, BF, *[None] * 9, None) == L.MOE_OK
+
+
+# ---- tensors that overlap --------------------------------------------------
+def outputs_are_distinct(out, counts, types, sources, norm=0):
+    import numpy as np
+    pack = lambda v, t: np.array(v, t).tobytes()  # noqa: E731
+    return L.tensors().distinct(pack(out, np.uint64), pack(counts, np.int64), pack(types, np.int32),
+                                pack(sources, np.uint64), norm)
+
+
+def test_outputs_that_overlap_are_found():
+    bf, f = 1, 0  # describe's types
+    yes = outputs_are_distinct
+    assert yes([100, 200], [50, 50], [bf, bf], [100, 200])          # in place, end to end
+    assert not yes([100, 198], [50, 50], [bf, bf], [100, 198])      # one element shared
+    assert not yes([100, 200], [26, 50], [f, bf], [100, 200])       # fp32 elements are four bytes
+    assert not yes([100, 120], [50, 2], [bf, bf], [100, 120])       # one inside the other
+    assert yes([100, 100, 120], [50, 0, 0], [bf] * 3, [100, 0, 0])  # empty tensors overlap nothing
+    # into other tensors
+    assert yes([1000, 1100], [50, 50], [bf, bf], [100, 200])
+    assert yes([1000, 1100], [50, 50], [bf, bf], [100, 100])        # a gradient read twice
+    assert yes([100, 1100], [50, 50], [bf, bf], [100, 200])         # one of them in place
+    assert not yes([200, 100], [50, 50], [bf, bf], [100, 200])      # the gradients in another order
+    assert not yes([102, 1100], [50, 50], [bf, bf], [100, 200])     # shifted by an element
+    assert not yes([1000, 298], [50, 50], [bf, bf], [100, 200])     # its own gradient's last element
+    assert not yes([1000, 198], [50, 2], [bf, bf], [100, 300])      # another's last element
+    assert not yes([100, 140], [20, 20], [bf, bf], [100, 139])      # its own and another output
+    assert yes([], [], [], [])
+    # the norm
+    assert not yes([100], [50], [bf], [100], 196)
+    assert yes([100], [50], [bf], [100], 200) and yes([100], [50], [bf], [100], 96)
+    with pytest.raises(TypeError):
+        L.tensors().distinct(b"", b"", b"")
+    with pytest.raises(TypeError):
+        L.tensors().distinct(bytes(8), bytes(8), bytes(8), bytes(8), 0)  # types are four bytes each
+
+
+def test_overlap_against_every_pair():
+    import random
+    rng = random.Random(3)
+    found = 0
+    for _ in range(3000):
+        n = rng.randint(1, 4)
+        counts, types = [rng.randint(0, 4) for _ in range(n)], [rng.randint(0, 1) for _ in range(n)]
+        size = [c * (2 if t else 4) for c, t in zip(counts, types)]
+        src = [rng.randrange(0, 200, 2) for _ in range(n)]
+        out = [s if rng.random() < 0.3 else rng.randrange(0, 200, 2) for s in src]
+        norm = rng.randrange(4, 200, 4)
+
+        def meet(a, na, b, nb):
+            return na > 0 and nb > 0 and a < b + nb and b < a + na
+        good = not any(meet(out[i], size[i], norm, 4) for i in range(n))
+        for i in range(n):
+            for j in range(n):
+                good &= i == j or not meet(out[i], size[i], out[j], size[j])
+                good &= (i == j and out[i] == src[i]) or not meet(out[i], size[i], src[j], size[j])
+        assert outputs_are_distinct(out, counts, types, src, norm) == good
+        found += not good
+    assert 300 < found < 2700

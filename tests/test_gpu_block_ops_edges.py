@@ -35,3 +35,21 @@ def test_empty_batch_of_the_weighted_sums_gradient(need_do, need_dw):
                                       need_do=need_do, need_dw=need_dw)
     assert (do.shape == (0, 24)) if need_do else do is None
     assert (dw.shape == (0, 2)) if need_dw else dw is None
+
+
+# ---- tensors that overlap (refused before anything is launched) -------------
+def test_clip_refuses_tensors_that_overlap():
+    t = torch.ones(100, device="cuda")
+    keep, norm = t.clone(), torch.ones(1, device="cuda")
+    a, b = t[:50], t[50:]
+    for grads, kw in [([t, t[10:20]], {}), ([t[:60], t[40:]], {}), ([a, b], dict(out=[b, a])),
+                      ([a, b], dict(out=[t[1:51], torch.empty(50, device="cuda")])), ([a, b], dict(out=[a, t[25:75]])),
+                      ([norm, a], dict(norm=norm))]:
+        with pytest.raises(ValueError):
+            M.clip_grads(grads, 1.0, **kw)
+    assert torch.equal(t, keep)
+    # views side by side, and one gradient into two outputs
+    M.clip_grads([a, b], 5.0)
+    assert bool((t - 0.5).abs().max() < 1e-6)
+    out, n = M.clip_grads([a, a], 1e9, out=[torch.empty(50, device="cuda") for _ in range(2)])
+    assert abs(float(n) - 5.0) < 1e-5 and all(torch.equal(o, a) for o in out)
