@@ -220,10 +220,11 @@ class BlockNormPlan(_BlockPlan):
     without a block output), a [T][d] (None with pre_norm=False), r_post and
     r_pre [T] for the backward."""
 
-    def __init__(self, block: Block, device="cuda", pre_norm=True):
+    def __init__(self, block: Block, device="cuda", pre_norm=True, output=True):
+        """output=False: a step without a block output (no x_out)."""
         super().__init__(block, device)
         T, d, dev = block.T, block.d, self.device
-        self.x_out = torch.empty(T, d, dtype=block.res, device=dev)
+        self.x_out = torch.empty(T, d, dtype=block.res, device=dev) if output else None
         self.a = torch.empty(T, d, dtype=block.act, device=dev) if pre_norm else None
         self.r_pre = torch.empty(T, dtype=torch.float32, device=dev) if pre_norm else None
         self.r_post = torch.empty(T, dtype=torch.float32, device=dev) if block.post_norm else None
@@ -234,7 +235,8 @@ class BlockNormPlan(_BlockPlan):
         _need("x", x)
         px, py = _check("x", x, self._res, self._rows, dev), _check("y", y, self._act, self._rows, dev)
         _launch(dev, "moe_block_norm", self.cblock, self._prec, px, py, *self._vectors(w_pre, w_post, gate),
-                None if y is None else self.x_out.data_ptr(), None if self.a is None else self.a.data_ptr(),
+                None if y is None or self.x_out is None else self.x_out.data_ptr(),
+                None if self.a is None else self.a.data_ptr(),
                 None if self.r_post is None else self.r_post.data_ptr(),
                 None if self.r_pre is None else self.r_pre.data_ptr())
         return (x if y is None else self.x_out), self.a
@@ -243,7 +245,7 @@ class BlockNormPlan(_BlockPlan):
 def block_norm(block: Block, x, y=None, w_pre=None, w_post=None, gate=None, pre_norm=True):
     """moe_block_norm into fresh tensors: (x_out, a, plan); the plan keeps
     r_pre and r_post for block_norm_backward."""
-    plan = BlockNormPlan(block, _need("x", x), pre_norm)
+    plan = BlockNormPlan(block, _need("x", x), pre_norm, y is not None)
     return plan.run(x, y, w_pre, w_post, gate) + (plan,)
 
 

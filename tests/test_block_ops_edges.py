@@ -95,3 +95,12 @@ def test_overlap_against_every_pair():
         assert outputs_are_distinct(out, counts, types, src, norm) == good
         found += not good
     assert 300 < found < 2700
+
+
+# ---- plans -----------------------------------------------------------------
+def test_norm_plan_without_a_block_output():
+    """The step before the first block keeps no second residual."""
+    block = M.Block(4, 8, post_norm=True)
+    plan = M.BlockNormPlan(block, device="cpu", output=False)
+    assert plan.x_out is None and plan.a.shape == (4, 8)
+    assert M.BlockNormPlan(block, device="cpu").x_out.shape == (4, 8)

@@ -53,3 +53,17 @@ def test_clip_refuses_tensors_that_overlap():
     assert bool((t - 0.5).abs().max() < 1e-6)
     out, n = M.clip_grads([a, a], 1e9, out=[torch.empty(50, device="cuda") for _ in range(2)])
     assert abs(float(n) - 5.0) < 1e-5 and all(torch.equal(o, a) for o in out)
+
+
+# ---- plans -----------------------------------------------------------------
+def test_norm_without_a_block_output_keeps_no_residual():
+    x, y = torch.ones(3, 64, device="cuda"), torch.ones(3, 64, device="cuda")
+    block = M.Block(3, 64, "f32")
+    same, a, plan = M.block_norm(block, x)
+    assert same is x and plan.x_out is None
+    x_out, b, whole = M.block_norm(block, x, torch.zeros_like(y))
+    assert whole.x_out is x_out and torch.equal(x_out, x) and torch.equal(a, b)
+    with pytest.raises(M._lib.MoeError):  # a block output has nowhere to go
+        plan.run(x, y)
+    again, b = plan.run(x)
+    assert again is x and b is plan.a and torch.equal(a, b)
