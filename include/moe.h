@@ -240,7 +240,9 @@ moe_status moe_shared_ffn(const moe_dims* dims, moe_prec prec, const void* x, co
  *   y[t] = sum_{j ascending expert} topk_w[t][j] * o_perm[token_row[t][j]]
  *          + y_shared[t]
  * accumulated in fp32 in that fixed order, rounded once to the output type.
- * y_shared may be NULL.  Tensors in the activation type (bf16 in MXFP8). */
+ * y_shared may be NULL.  Tensors in the activation type (bf16 in MXFP8).
+ * Every token_row entry must be a row in [0, R), as moe_permute writes it: a
+ * schedule with absent routes (moe_sort_tokens) goes to moe_unsort_tokens. */
 moe_status moe_combine(const moe_dims* dims, moe_prec prec, const void* o_perm, const int32_t* token_row,
                        const float* topk_w, const void* y_shared, void* y, void* stream);
 
@@ -276,7 +278,9 @@ moe_status moe_layer_forward(const moe_dims* dims, moe_prec prec, const void* x,
  * zero-padded to a multiple of 128); the shared expert and the router stay
  * bf16.  MOE_F32 returns MOE_EUNSUPPORTED.  Every reduction runs in a fixed
  * order (results are bitwise reproducible); experts without rows get exact
- * zero weight gradients.  ws: workspace of moe_workspace_bytes(which=4). */
+ * zero weight gradients.  Every route must be present: token_row indexes the
+ * routed rows unchecked, so a schedule of moe_sort_tokens with absent routes
+ * must not be passed.  ws: workspace of moe_workspace_bytes(which=4). */
 moe_status moe_layer_backward(const moe_dims* dims, moe_prec prec, const void* dy, const void* x,
                               const moe_weights* w, const moe_routing* routing, void* dx, const moe_grads* g,
                               void* ws, size_t ws_bytes, void* stream);
@@ -385,7 +389,10 @@ moe_status moe_bf16_mma_tiles(const void* a, const void* b, const float* c, floa
  * moe_permute and moe_combine for callers whose routes may be absent, with
  * the gradients of both: a route whose expert id lies outside [0, E) is
  * absent (a padding token, a dropped route, an expert of another rank, whose
- * ids become local by subtracting the rank's first expert).  Of `dims` only
+ * ids become local by subtracting the rank's first expert).  Absent routes
+ * have token_row -1, which only the calls of this section take; moe_combine
+ * and moe_layer_backward need every route present.  The rows of the present
+ * routes can go through moe_expert_ffn.  Of `dims` only
  * T, d, k and, in moe_sort_tokens, E are read: T <= 4,194,303,
  * 1 <= d <= 2^30, 1 <= k <= 16 (k may exceed E), E <= 1024.  MOE_F32 and
  * MOE_BF16; rows need element alignment only.  Indices are int32.  Outputs

@@ -113,7 +113,9 @@ class SortPlan:
 def sort_tokens(topk_idx, x, dims: Dims, prec: str, gather=True):
     """moe_sort_tokens into fresh tensors: (counts, offsets, row_token,
     token_row, x_perm).  row_token and x_perm hold nothing of use from row
-    offsets[E] on."""
+    offsets[E] on.  token_row is -1 for an absent route, which unsort_tokens
+    and the gradients here take and combine and layer_backward must not be
+    given."""
     return SortPlan(dims, prec, _need("topk_idx", topk_idx), gather=gather).run(topk_idx, x)
 
 

@@ -179,6 +179,8 @@ def shared_ffn(x, weights: Weights, dims: Dims, prec: str):
 
 
 def combine(o_perm, token_row, topk_w, y_shared, dims: Dims, prec: str):
+    """moe_combine.  token_row as permute gives it, every route present; with
+    absent routes: unsort_tokens."""
     y = torch.empty(dims.T, dims.d, dtype=_act_dtype(prec), device=token_row.device)
     call("moe_combine", ctypes.byref(dims.c()), PREC[prec], _p(o_perm), _p(token_row), _p(topk_w), _p(y_shared), _p(y),
          _stream())
@@ -363,6 +365,8 @@ class BackwardPlan:
 
 
 def layer_backward(dy, x, weights: Weights, routing, dims: Dims, prec: str, router_grad=True):
+    """moe_layer_backward into fresh tensors: (dx, grads).  routing as
+    layer_forward gives it, every route present."""
     plan = BackwardPlan(dims, prec, dy.device, router_grad)
     return plan.run(dy, x, weights, routing)
 
