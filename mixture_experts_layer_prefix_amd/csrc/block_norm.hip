@@ -19,8 +19,11 @@
 // every row once and are bound by memory.  A slot is 16 bytes of the residual,
 // so that one instruction of a wave covers whole cache lines: fp32 in slots of
 // 32 bytes, each access filling half of its lines, took 106 us for 8,192 x
-// 4,096 forward, in 16 bytes 83.  The forward's outputs are written with the
-// streaming hint (8,192 x 7,168 bf16: 98 us without, 78 with).
+// 4,096 forward, in 16 bytes 83.  The forward's outputs are always written
+// with the streaming hint.  8,192 x 7,168 bf16 on new inputs: 88 us, 93
+// without; two such steps, the second reading the first's outputs: 177 and
+// 186.  Where the caches hold the outputs the reader pays for it: two steps of
+// 2,048 rows 52 and 51 us, of 1,024 rows 29.0 and 27.8; of 1 and 64 no change.
 #include <type_traits>
 
 #include "block_norm.h"
@@ -77,8 +80,8 @@ __device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, fl
 // serves them.  w_pre and c = beta gate w_post stay in the threads' registers
 // (MANY, several gate rows: c without the gate, whose row is read each time):
 // read anew for every row they would be 12 bytes a channel from L2 beside the
-// row's 8 bytes from memory (126 us for 8,192 x 7,168 bf16; so 95, and 88 with
-// streaming writes: 5.3 TB/s).  TAIL: d is not a multiple of the slot.
+// row's 8 bytes from memory (126 us for 8,192 x 7,168 bf16; so 93, and 88 with
+// the writes streamed: 5.3 TB/s).  TAIL: d is not a multiple of the slot.
 template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
 __global__ void __launch_bounds__(1024, VPT * kPer<RF32> <= 8 ? 8 : 4) block_norm_kernel(BlockNorm p) {
   constexpr int N = kPer<RF32>;
@@ -190,8 +193,11 @@ template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL, bool STREAM>
 __global__ void __launch_bounds__(1024) block_norm_bwd_kernel(BlockNormBwd p) {
   constexpr int N = kPer<RF32>, Q = N / 4;
   // Up to eight channels a thread the column sums are in registers, and cols
-  // is room to add the teams' sums; for sixteen they are in LDS, as
-  // [sum][slot][quarter][thread], each thread touching its own only.
+  // is room to add the teams' sums; for sixteen (rows above 8,192 channels)
+  // they are in LDS, as [sum][slot][quarter][thread], each thread touching its
+  // own only.  All instances of sixteen still spill at 128 registers: 8 to 56
+  // of bf16, 22 to 99 with an fp32 residual, 38 to 129 of fp32.  4,096 x 12,288
+  // with both norms and a gate: 140, 227 and 343 us (floors 120, 180, 240).
   constexpr bool REG = VPT * N <= 8;
   __shared__ float red[2][16][3];
   __shared__ f32x4 cols[(REG ? 1 : 2 * VPT) * Q * 1024];

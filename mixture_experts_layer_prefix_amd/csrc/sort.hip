@@ -15,8 +15,9 @@
 // thread a 16-byte slot of it, and the token's row numbers are scalars.  On
 // new inputs, bf16: sort of 8,192 x 7,168 with k = 8, an eighth of the tokens
 // absent, 197 us (4.8 TB/s, 14 us of it the schedule); unsort of 16,384 x
-// 6,144 with one route in eight present 98 us (6.2 TB/s); unsort backward of
-// 8,192 x 4,096 with k = 8 209 us (5.5 TB/s).  A copy reaches 5.0 TB/s.
+// 6,144 with one route in eight present 95 to 103 us (about 6 TB/s); unsort
+// backward of 8,192 x 4,096 with k = 8 209 us (5.5 TB/s).  A copy reaches 5.0
+// TB/s.
 #include <type_traits>
 
 #include "rows.h"
@@ -383,7 +384,9 @@ __global__ void __launch_bounds__(1024) unsort_kernel(const void* __restrict__ r
 }
 
 // dy's slot is read once for all routes, o's rows stream through and so do the
-// gradient's (8,192 x 4,096, k = 8: 232 us without the hint on the writes, 209).
+// gradient's (8,192 x 4,096, k = 8: 231 us without the hint on the writes,
+// 209).  A kernel that reads those rows next pays for it: with the sort's
+// backward after it 312 us, 299 without the hint; 1,024 x 7,168 81 and 74.
 // Weights (dov) and rows of o (dw) are read only for the output they serve.
 template <bool F32, bool TAIL>
 __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict__ dy, const void* __restrict__ o,
@@ -443,9 +446,11 @@ __global__ void __launch_bounds__(1024) unsort_bwd_kernel(const void* __restrict
   }
 }
 
-// Rows that the last cache level (256 MB) holds little of are read and written
-// with the streaming hint; smaller ones are likely to be in it, having just
-// been written, or to be read from it next.
+// Rows that the last cache level (256 MB) holds little of are read with the
+// streaming hint; smaller ones are likely to be in it, having just been
+// written.  The rule is on the buffer's T * k rows: which of them are present
+// is known on the device only.  A present eighth is not slower for it: 59 MB of
+// a 470 MB buffer 32.3 us, 33.6 without the hint; 117 MB of 940 MB 62.0, 63.3.
 bool beyond_caches(bool f32, int64_t rows, int d) { return rows * d * (f32 ? 4 : 2) > (384ll << 20); }
 
 // The instance of a kernel for an element type, a row length and a hint:
@@ -465,14 +470,30 @@ auto row_kernel(bool f32, int d, bool stream, Pick pick) {
 
 }  // namespace
 
-// Which schedule: kernel times in us for 256 experts and k = 8; "few" holds
-// the copy of the rows, whose own kernel takes 3.0 (d = 512) to 11.3 (d = 7168,
-// 4,096 routes) beside the others, and each further launch costs about 1 us.
-//   routes               512    2,048     4,096      32,768  65,536  131,072
-//   few   d = 512/7168   5/6.4  8.8/10.4  13.9/20.8
-//   wide                 4.6    5.0       5.3        9.0     15.1    20
-//   count, scan, rank    8.6    9.8       10.4       13      15      16
-// Whole calls at 65,536 routes (d = 7168): wide 200, count, scan, rank 197.
+// Which schedule.  Device times in us of whole calls, one after another
+// (k = 8; 1 expert: k = 1).  With the rows of 512 or 7,168 channels, 256
+// experts:
+//   routes                512        2,048      4,096
+//   few                   4.4 / 5.8  8.2 / 11   13.4 / 20.9
+//   wide                  6.4 / 8.2  6.8 / 11   7.2 / 16.5
+//   count, scan, rank     10 / 12    11 / 15    12 / 21
+// The schedule alone (no rows):
+//   routes                512   2,048   4,096   16,384   32,768   65,536
+//   few, 8 or more        3.8   7.4     12.4
+//     1                   3.4   8.7     21.2
+//   wide, 1,024 experts   4.0   4.2     4.4     5.5      6.8      9.8
+//     256                 3.9   4.2     4.5     5.6      6.9      9.6
+//     8                   4.0   4.2     4.6     7.0      10.3     16.7
+//     1                   4.1   5.4     7.2     17.7     31.5     59.3
+//   three, 1,024 experts  9.0   9.9     10.1    11.0     12.1     14.2
+//     256                 8.1   8.5     8.8     9.5      10.1     10.9
+//     8                   7.5   7.7     8.1     8.4      8.5      8.7
+//     1                   6.8   7.5     7.5     7.6      7.7      7.9
+// The limits suit 64 experts and more with the rows copied (65,536 routes of
+// 256 experts with rows of 7,168: wide 200, three launches 197).  They are not
+// the best for a schedule alone of 2,048 routes (few, where wide is 3 us
+// faster), nor for 16,384 to 32,768 routes of very few experts, whose LDS
+// counters collide (wide, where three launches are up to 24 us faster).
 constexpr int64_t kFewRoutes = 2048, kWideLimit = 32768;
 
 size_t sort_scratch_bytes(int64_t T, int k, int E) {
@@ -522,8 +543,10 @@ hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, c
                          int64_t T, int d, int k, hipStream_t s) {
   if (T == 0) return hipSuccess;
   const RowShape g = row_shape(f32, T, d);
-  // 65,536 bf16 rows of 7,168: 215 us, streaming 196; of 4,096: 121, 109; of
-  // 1,536: 37.7, 41.3.  The sums are streamed in any case: 226 us without.
+  // 65,536 bf16 rows of 7,168 without an addend: 199 us, streaming 189; of
+  // 4,096: 110, 102; of 1,536: 44.4, 40.5 from memory, but 37.7, 41.3 where the
+  // last cache level holds them.  The sums are streamed in any case: 206 us
+  // for 7,168 without.
   const auto kernel = row_kernel(f32, d, beyond_caches(f32, T * k, d), [](auto F32, auto TAIL, auto STREAM) {
     return unsort_kernel<F32.value, TAIL.value, STREAM.value>;
   });
