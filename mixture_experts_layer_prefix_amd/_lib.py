@@ -51,6 +51,13 @@ class moe_block(ctypes.Structure):
                 ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+def check_sizes(T, *sizes):
+    """Raises for sizes that moe_dims and moe_block would cut to 64 bits (T)
+    and 32 bits (the others): ctypes does so without a word."""
+    if not -1 << 63 <= T < 1 << 63 or any(not -1 << 31 <= n < 1 << 31 for n in sizes):
+        raise ValueError("T must fit in 64 bits and the other sizes in 32, not %s" % ((T,) + sizes,))
+
+
 _P = ctypes.c_void_p
 _DIMS = ctypes.POINTER(moe_dims)
 _BLOCK = ctypes.POINTER(moe_block)

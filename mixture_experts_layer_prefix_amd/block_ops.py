@@ -182,6 +182,10 @@ class Block:
     eps: float = 1e-6
     gate_every: int = 0
 
+    def __post_init__(self):
+        _lib.check_sizes(self.T, self.d)
+        _lib.check_sizes(self.gate_every)
+
     @property
     def every(self):
         return self.gate_every or max(self.T, 1)

@@ -21,6 +21,9 @@ class Dims:
     S: int = 0
     Is: int = 0
 
+    def __post_init__(self):
+        _lib.check_sizes(self.T, self.d, self.E, self.k, self.I, self.S, self.Is)
+
     def c(self):
         return moe_dims(self.T, self.d, self.E, self.k, self.I, self.S, self.Is if self.S else 0)
 

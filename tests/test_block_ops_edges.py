@@ -104,3 +104,16 @@ def test_norm_plan_without_a_block_output():
     plan = M.BlockNormPlan(block, device="cpu", output=False)
     assert plan.x_out is None and plan.a.shape == (4, 8)
     assert M.BlockNormPlan(block, device="cpu").x_out.shape == (4, 8)
+
+
+# ---- sizes that the C structs cannot hold ----------------------------------
+@pytest.mark.parametrize("make", [
+    lambda: M.Dims(1, (1 << 32) + 64, 8, 1, 1), lambda: M.Dims(1, 64, (1 << 32) + 8, 1, 1),
+    lambda: M.Dims(1, 64, 8, (1 << 32) + 1, 1), lambda: M.Dims((1 << 64) + 1, 64, 8, 1, 1),
+    lambda: M.Dims(1, 1 << 31, 8, 1, 1), lambda: M.Block(1, (1 << 32) + 64), lambda: M.Block((1 << 64) + 1, 64),
+    lambda: M.Block(1, 64, gate_every=1 << 64)])
+def test_sizes_are_not_cut(make):
+    """ctypes keeps the low bits: 2^32 + 64 channels would have run as 64."""
+    with pytest.raises(ValueError):
+        make().c()
+    assert M.Dims(5, (1 << 31) - 1, 8, 1, 1).c().d == (1 << 31) - 1
