@@ -467,7 +467,8 @@ moe_status moe_block_norm(const moe_block* block, moe_prec prec, const void* x, 
                           void* stream);
 
 /* Backward from the gradients of x' (dx_out) and a (da), either NULL where
- * there is none, the forward's x', y, r_post and r_pre:
+ * there is none, the forward's x', y, r_post and r_pre (without da, r_pre and
+ * w_pre are NULL):
  *   xh = x' r_pre, u = da w_pre, dz = dx_out + r_pre (u - xh mean(u xh))
  *   dx = alpha dz (dz without a block output), dw_pre = sum_t da xh
  *   e = beta dz, dn = e gate, dgate[g] = sum over its tokens of e n

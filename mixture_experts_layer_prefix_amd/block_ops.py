@@ -278,7 +278,8 @@ class BlockNormBackwardPlan(_BlockPlan):
 
     def run(self, dx_out, da, x_out, y, r_pre, r_post, w_pre=None, w_post=None, gate=None):
         """(dx, dy, grads) from the gradients of x_out and a (None: no
-        gradient), the forward's x_out, y and row statistics."""
+        gradient), the forward's x_out, y and row statistics (without da, r_pre
+        and w_pre are None)."""
         dev, rows, tokens, f32 = self.device, self._rows, (self.block.T,), torch.float32
         _need("dx_out or da", da if dx_out is None else dx_out)
         args = (_check("dx_out", dx_out, self._res, rows, dev), _check("da", da, self._act, rows, dev),
