@@ -135,7 +135,8 @@ const char* moe_status_str(moe_status s);
 
 /* Workspace needed by an entry point: which = 0 moe_layer_forward,
  * 1 moe_permute, 2 moe_expert_ffn, 3 moe_shared_ffn, 4 moe_layer_backward,
- * 5 moe_sort_tokens (only T, d, E and k are read, within that call's limits).
+ * 5 moe_sort_tokens (only T, d, E and k are read, within that call's limits),
+ * 6 moe_routed_ffn_mxfp4 (within that call's limits; prec is not read).
  * Writes the byte count to *bytes (host pointer).  Pure host computation. */
 moe_status moe_workspace_bytes(const moe_dims* dims, moe_prec prec, int which, size_t* bytes);
 
@@ -410,6 +411,19 @@ moe_status moe_sort_tokens(const moe_dims* dims, moe_prec prec, const int32_t* t
                            int32_t* expert_counts, int32_t* expert_offsets, int32_t* row_token, int32_t* token_row,
                            void* x_perm, void* ws, size_t ws_bytes, void* stream);
 
+/* moe_sort_tokens of tokens that are in 8 bits already (moe_block_norm_mxfp8):
+ * x [T][d] E4M3 codes with x_scale [T][d/32] E8M0 into x_perm [T*k][d] and
+ * x_perm_scale [T*k][d/32], byte for byte: the rows that moe_expert_ffn and
+ * moe_expert_gate_up take in MOE_MXFP8.  d must be a multiple of 32 (else
+ * MOE_EUNSUPPORTED); codes are 16-byte and scales 4-byte aligned.  The
+ * schedule, absent routes and the workspace (which = 5, any prec that
+ * moe_sort_tokens takes) are those of moe_sort_tokens; outputs past row
+ * expert_offsets[E] are not written. */
+moe_status moe_sort_tokens_mxfp8(const moe_dims* dims, const int32_t* topk_idx, const uint8_t* x,
+                                 const uint8_t* x_scale, int32_t* expert_counts, int32_t* expert_offsets,
+                                 int32_t* row_token, int32_t* token_row, uint8_t* x_perm, uint8_t* x_perm_scale,
+                                 void* ws, size_t ws_bytes, void* stream);
+
 /* Gradient of x_perm with respect to x:
  *   dx[t] = sum_{j present} dx_perm[token_row[t][j]] + dx_add[t],
  * fp32 in slot order, rounded once.  dx_add may be NULL.  A token_row entry
@@ -486,6 +500,17 @@ moe_status moe_block_norm_backward(const moe_block* block, moe_prec prec, const 
                                    float* dw_post, float* dgate, float* dw_pre, void* ws, size_t ws_bytes,
                                    void* stream);
 
+/* moe_block_norm in MOE_BF16 with a in 8 bits: a_q [T][d] E4M3 codes and
+ * a_scale [T][d/32] E8M0 scales, those that moe_quantize_mxfp8 (axis 0) makes
+ * of the bf16 a, bit for bit; the layout that moe_permute gives its rows in
+ * MOE_MXFP8.  a [T][d] bf16 (for the router and a shared expert) may be NULL.
+ * d must be a multiple of 32 (else MOE_EUNSUPPORTED); a_q is 16-byte aligned.
+ * Neither a_q nor a_scale may be NULL.  The rest is as in moe_block_norm,
+ * whose backward serves this step too (with the gradient of a). */
+moe_status moe_block_norm_mxfp8(const moe_block* block, const void* x, const void* y, const float* w_post,
+                                const float* gate, const float* w_pre, void* x_out, void* a, uint8_t* a_q,
+                                uint8_t* a_scale, float* r_post, float* r_pre, void* stream);
+
 /* ---- Gradient norm and clipping -------------------------------------------
  * n tensors: grads (HOST array of device pointers), numel (HOST array of
  * element counts), types (HOST array: MOE_F32 or MOE_BF16 each).  Pointers need
@@ -512,6 +537,53 @@ moe_status moe_grad_norm(const void* const* grads, const int64_t* numel, const i
 moe_status moe_clip_grads(const void* const* grads, void* const* out, const int64_t* numel, const int32_t* types,
                           int32_t n, float max_norm, const float* norm_in, float* norm, void* ws, size_t ws_bytes,
                           void* stream);
+
+/* ---- Experts in 4 bits for a few tokens ------------------------------------
+ * MXFP4 matrices (OCP MX v1.0): E2M1 elements, two to a byte (element 2i of a
+ * row in the low half of byte i), with one E8M0 scale per 32 elements of a
+ * row, stored slab-major like the MXFP8 weights': scale [cols/128][rows][4],
+ * byte (c/128, r, (c/32) % 4) for the block of row r holding column c.
+ *
+ * moe_quantize_mxfp4: of a bf16 matrix [rows][cols] (cols a multiple of 128,
+ * at most 2^24; rows at most 2^28 - 16).  Per block: e = the smallest integer
+ * with max |v| / 2^e <= 6, clamped to [-127, 127] (-127 for an all-zero
+ * block); element = v / 2^e rounded to nearest-even E2M1, sign kept; scale
+ * byte = e + 127.  dst [rows][cols/2].
+ * moe_dequantize_mxfp4: back to bf16, each value once rounded (exact but below
+ * bf16's normal numbers), for products with many rows (moe_layer_forward,
+ * moe_quantize_mxfp8) from the same weights. */
+moe_status moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* dst, uint8_t* scale,
+                              void* stream);
+moe_status moe_dequantize_mxfp4(const uint8_t* src, const uint8_t* scale, int64_t rows, int64_t cols, void* dst_bf16,
+                                void* stream);
+
+/* Routed experts as MXFP4 matrices (host struct of device pointers): codes
+ * [E][rows][cols/2] and scales [cols/128][E*rows][4] of the stacked
+ * [E*rows][cols] matrix, I rows of d columns for gate and up, d rows of I
+ * columns for down. */
+typedef struct {
+  const uint8_t *q_gate, *q_gate_scale;
+  const uint8_t *q_up, *q_up_scale;
+  const uint8_t *q_down, *q_down_scale;
+} moe_weights_mxfp4;
+
+/* The routed experts of a few tokens, from tokens to the weighted sum:
+ *   h = MX(SiLU(x_t W_g[e]^T) * (x_t W_u[e]^T)),  e = topk_idx[t][j],
+ *   y[t] = sum_j topk_w[t][j] h W_d[e]^T + y_add[t]
+ * with x [T][d] E4M3 and x_scale [T][d/32] E8M0 (moe_block_norm_mxfp8,
+ * moe_quantize_mxfp8 axis 0), h rounded to E4M3 with a scale per 32 columns as
+ * in MOE_MXFP8, fp32 accumulation, y [T][d] bf16 rounded once.  y_add bf16 or
+ * NULL; it may be y.  A route whose id is outside [0, E) (padding, a dropped
+ * route, another rank's expert) adds nothing, whatever its weight holds; a
+ * token without routes gives y_add or zeros.  An id may come more than once.
+ * A token's result does not depend on the others of its batch.
+ * Only T, d, E, k and I of dims are read: d and I multiples of 128, I * d below
+ * 2^32, T <= 4,194,303, 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E).  Any T
+ * is computed; from some hundred routes an expert on moe_expert_ffn is
+ * faster.  ws: moe_workspace_bytes(which = 6) bytes. */
+moe_status moe_routed_ffn_mxfp4(const moe_dims* dims, const uint8_t* x, const uint8_t* x_scale,
+                                const int32_t* topk_idx, const float* topk_w, const moe_weights_mxfp4* w,
+                                const void* y_add, void* y, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

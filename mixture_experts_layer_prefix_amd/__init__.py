@@ -12,3 +12,5 @@ from .ops import (Dims, Weights, ForwardPlan, route, permute, permute_noalloc, e
 from .block_ops import (Block, BlockNormPlan, BlockNormBackwardPlan, SortPlan, block_norm, block_norm_backward,  # noqa: F401
                         clip_grads, grad_norm, sort_tokens, sort_tokens_backward, unsort_tokens,
                         unsort_tokens_backward)
+from .mx_ops import (BlockNormMxfp8Plan, RoutedFfnPlan, SortMxfp8Plan, WeightsMxfp4, block_norm_mxfp8,  # noqa: F401
+                     dequantize_mxfp4, prepare_mxfp4, quantize_mxfp4, routed_ffn_mxfp4, sort_tokens_mxfp8)

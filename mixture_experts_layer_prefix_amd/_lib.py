@@ -51,6 +51,11 @@ class moe_block(ctypes.Structure):
                 ("beta", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class moe_weights_mxfp4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "q_gate", "q_gate_scale", "q_up", "q_up_scale", "q_down", "q_down_scale")]
+
+
 def check_sizes(T, *sizes):
     """Raises for sizes that moe_dims and moe_block would cut to 64 bits (T)
     and 32 bits (the others): ctypes does so without a word."""
@@ -99,6 +104,12 @@ _SIGS = {
     "moe_grad_norm": ([_P, _P, _P, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "moe_clip_grads": ([_P, _P, _P, _P, ctypes.c_int32, ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P],
                        ctypes.c_int),
+    "moe_block_norm_mxfp8": ([_BLOCK] + [_P] * 12, ctypes.c_int),
+    "moe_sort_tokens_mxfp8": ([_DIMS] + [_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_quantize_mxfp4": ([_P, ctypes.c_int64, ctypes.c_int64, _P, _P, _P], ctypes.c_int),
+    "moe_dequantize_mxfp4": ([_P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P], ctypes.c_int),
+    "moe_routed_ffn_mxfp4": ([_DIMS] + [_P] * 4 + [ctypes.POINTER(moe_weights_mxfp4)] + [_P] * 3 +
+                             [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_bf16_mma_tiles": ([_P, _P, _P, _P, ctypes.c_int64, _P], ctypes.c_int),
 }
 

@@ -4,20 +4,16 @@
 #include <math.h>
 
 #include "block_norm.h"
+#include "checks.h"
 #include "clip.h"
 
 using namespace moe;
 
 namespace {
 
-// Workgroups times threads of a launch stay below 2^32.
-constexpr int64_t kMaxTokens = 4194303;
 constexpr int kMaxNormDim = 16384;
 // The row kernels count columns in an int, in steps of at most 8,192.
 constexpr int kMaxRowDim = 1 << 30;
-
-bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool need(const void* p, size_t n) { return p && aligned_to(p, n); }
 
 size_t elem(moe_prec prec) { return prec == MOE_F32 ? 4 : 2; }
 
@@ -51,18 +47,43 @@ moe_status check_grads(const void* const* grads, const int64_t* numel, const int
   return MOE_OK;
 }
 
-moe_status check_scratch(const void* ws, size_t bytes, size_t required) {
-  if (required && (!ws || bytes < required)) return MOE_EWORKSPACE;
-  return aligned_to(ws, 16) ? MOE_OK : MOE_EINVAL;
+// moe_block_norm, and moe_block_norm_mxfp8 with a_q.
+moe_status block_norm(const moe_block* block, moe_prec prec, const void* x, const void* y, const float* w_post,
+                      const float* gate, const float* w_pre, void* x_out, void* a, uint8_t* a_q, uint8_t* a_scale,
+                      float* r_post, float* r_pre, void* stream) {
+  MOE_TRY(check_block(block, prec, gate != nullptr));
+  if (block->T == 0) return MOE_OK;  // empty tensors may have no address
+  const bool norm = a || a_q;
+  if (!y && (!norm || x_out || gate || block->post_norm)) return MOE_EINVAL;
+  if ((w_post || r_post) && !block->post_norm) return MOE_EINVAL;
+  if ((w_pre || r_pre) && !norm) return MOE_EINVAL;
+  const size_t na = elem(prec), nr = block->res_f32 ? 4 : na;
+  if (!need(x, nr) || !aligned_to(y, na) || (y && !need(x_out, nr)) || !aligned_to(a, na)) return MOE_EINVAL;
+  for (const void* p : {(const void*)w_post, (const void*)gate, (const void*)w_pre, (const void*)r_post,
+                        (const void*)r_pre})
+    if (!aligned_to(p, 4)) return MOE_EINVAL;
+  BlockNorm p = {};
+  p.T = block->T;
+  p.gate_every = block->gate_every;
+  p.d = block->d;
+  p.post_norm = block->post_norm != 0;
+  p.alpha = block->alpha;
+  p.beta = block->beta;
+  p.eps = block->eps;
+  p.x = x;
+  p.y = y;
+  p.w_post = w_post;
+  p.gate = gate;
+  p.w_pre = w_pre;
+  p.x_out = x_out;
+  p.a = a;
+  p.a_q = a_q;
+  p.a_scale = a_scale;
+  p.r_post = r_post;
+  p.r_pre = r_pre;
+  return done(launch_block_norm(prec == MOE_F32, prec == MOE_F32 || block->res_f32, p,
+                                static_cast<hipStream_t>(stream)));
 }
-
-moe_status done(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
-
-#define MOE_TRY(expr)              \
-  do {                             \
-    moe_status st_ = (expr);       \
-    if (st_ != MOE_OK) return st_; \
-  } while (0)
 
 }  // namespace
 
@@ -91,6 +112,23 @@ moe_status moe_sort_tokens(const moe_dims* dims, moe_prec prec, const int32_t* t
   MOE_TRY(check_scratch(ws, ws_bytes, sort_scratch_bytes(dims->T, dims->k, dims->E)));
   return done(launch_sort(prec == MOE_F32, topk_idx, x, dims->T, dims->d, dims->E, dims->k, expert_counts,
                           expert_offsets, row_token, token_row, x_perm, ws, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_sort_tokens_mxfp8(const moe_dims* dims, const int32_t* topk_idx, const uint8_t* x,
+                                 const uint8_t* x_scale, int32_t* expert_counts, int32_t* expert_offsets,
+                                 int32_t* row_token, int32_t* token_row, uint8_t* x_perm, uint8_t* x_perm_scale,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  MOE_TRY(check_routes(dims, MOE_BF16, true));
+  if (dims->d % 32) return MOE_EUNSUPPORTED;
+  if (!need(expert_counts, 4) || !need(expert_offsets, 4)) return MOE_EINVAL;
+  if (dims->T > 0) {
+    if (!need(topk_idx, 4) || !need(row_token, 4) || !need(token_row, 4)) return MOE_EINVAL;
+    if (!need(x, 16) || !need(x_perm, 16) || x == x_perm) return MOE_EINVAL;
+    if (!need(x_scale, 4) || !need(x_perm_scale, 4) || x_scale == x_perm_scale) return MOE_EINVAL;
+  }
+  MOE_TRY(check_scratch(ws, ws_bytes, sort_scratch_bytes(dims->T, dims->k, dims->E)));
+  return done(launch_sort_mx(topk_idx, x, x_scale, dims->T, dims->d, dims->E, dims->k, expert_counts, expert_offsets,
+                             row_token, token_row, x_perm, x_perm_scale, ws, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_sort_tokens_backward(const moe_dims* dims, moe_prec prec, const void* dx_perm, const int32_t* token_row,
@@ -134,35 +172,16 @@ moe_status moe_unsort_tokens_backward(const moe_dims* dims, moe_prec prec, const
 moe_status moe_block_norm(const moe_block* block, moe_prec prec, const void* x, const void* y, const float* w_post,
                           const float* gate, const float* w_pre, void* x_out, void* a, float* r_post, float* r_pre,
                           void* stream) {
-  MOE_TRY(check_block(block, prec, gate != nullptr));
-  if (block->T == 0) return MOE_OK;  // empty tensors may have no address
-  if (!y && (!a || x_out || gate || block->post_norm)) return MOE_EINVAL;
-  if ((w_post || r_post) && !block->post_norm) return MOE_EINVAL;
-  if ((w_pre || r_pre) && !a) return MOE_EINVAL;
-  const size_t na = elem(prec), nr = block->res_f32 ? 4 : na;
-  if (!need(x, nr) || !aligned_to(y, na) || (y && !need(x_out, nr)) || !aligned_to(a, na)) return MOE_EINVAL;
-  for (const void* p : {(const void*)w_post, (const void*)gate, (const void*)w_pre, (const void*)r_post,
-                        (const void*)r_pre})
-    if (!aligned_to(p, 4)) return MOE_EINVAL;
-  BlockNorm p = {};
-  p.T = block->T;
-  p.gate_every = block->gate_every;
-  p.d = block->d;
-  p.post_norm = block->post_norm != 0;
-  p.alpha = block->alpha;
-  p.beta = block->beta;
-  p.eps = block->eps;
-  p.x = x;
-  p.y = y;
-  p.w_post = w_post;
-  p.gate = gate;
-  p.w_pre = w_pre;
-  p.x_out = x_out;
-  p.a = a;
-  p.r_post = r_post;
-  p.r_pre = r_pre;
-  return done(launch_block_norm(prec == MOE_F32, prec == MOE_F32 || block->res_f32, p,
-                                static_cast<hipStream_t>(stream)));
+  return block_norm(block, prec, x, y, w_post, gate, w_pre, x_out, a, nullptr, nullptr, r_post, r_pre, stream);
+}
+
+moe_status moe_block_norm_mxfp8(const moe_block* block, const void* x, const void* y, const float* w_post,
+                                const float* gate, const float* w_pre, void* x_out, void* a, uint8_t* a_q,
+                                uint8_t* a_scale, float* r_post, float* r_pre, void* stream) {
+  MOE_TRY(check_block(block, MOE_BF16, gate != nullptr));
+  if (block->d % 32) return MOE_EUNSUPPORTED;
+  if (block->T > 0 && (!need(a_q, 16) || !need(a_scale, 1))) return MOE_EINVAL;
+  return block_norm(block, MOE_BF16, x, y, w_post, gate, w_pre, x_out, a, a_q, a_scale, r_post, r_pre, stream);
 }
 
 size_t moe_block_norm_scratch_bytes(int64_t T, int32_t d) {

@@ -10,7 +10,8 @@ struct BlockNorm {
   float alpha, beta, eps;
   const void *x, *y;                    // residual; block output or null
   const float *w_post, *gate, *w_pre;   // each or null
-  void *x_out, *a;                      // a null: no norm of x'
+  void *x_out, *a;                      // a null: no norm of x' (or its codes alone)
+  uint8_t *a_q, *a_scale;               // E4M3 codes and block scales of the bf16 a, or both null
   float *r_post, *r_pre;                // each or null
 };
 

@@ -74,6 +74,30 @@ __device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, fl
   }
 }
 
+// Codes and block scale of the slot of a at channel e, which may lie behind the
+// row (then it holds zeros and nothing is written).  All lanes take part.
+template <int N>
+__device__ __forceinline__ void store_mx(const BlockNorm& p, int64_t t, int e, const Slot<false, N>& a) {
+  float v[N];
+  unpack_slot(a, v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  m = max(m, dpp_u32<0xB1>(m));                          // lane ^ 1
+  m = max(m, dpp_u32<0x4E>(m));                          // lane ^ 2
+  if constexpr (N == 4) m = max(m, dpp_u32<0x141>(m));   // the other four of eight lanes
+  const int be = mx_block_exp_bits(m);
+  const float inv = mx_inv_scale(be);
+  if (e >= p.d) return;
+  uint32_t* q = reinterpret_cast<uint32_t*>(p.a_q + t * p.d + e);
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const uint32_t c = e4m3x4_rne_sat(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv);
+    __builtin_nontemporal_store(c, q + i / 4);
+  }
+  if (e % 32 == 0) p.a_scale[t * (p.d / 32) + e / 32] = (uint8_t)(be + 127);
+}
+
 // Teams of blockDim.x threads (whole waves), blockDim.y of them in a
 // workgroup, VPT slots of a row per thread.  Team b takes the rows b, b + n,
 // ... of n teams, all teams of a workgroup in step, so that one barrier
@@ -82,7 +106,12 @@ __device__ __forceinline__ void load_vec(const float* v, int64_t e, int left, fl
 // read anew for every row they would be 12 bytes a channel from L2 beside the
 // row's 8 bytes from memory (126 us for 8,192 x 7,168 bf16; so 93, and 88 with
 // the writes streamed: 5.3 TB/s).  TAIL: d is not a multiple of the slot.
-template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL>
+// MX (bf16 activations, d a multiple of 32): also the E4M3 codes of the
+// rounded a and a scale per 32 channels.  A block lies in the slots of four
+// neighbouring lanes (eight of four channels each), which find its largest
+// magnitude by exchanges inside a row of 16 lanes: no pass of its own, and a
+// is not read back.
+template <bool AF32, bool RF32, int VPT, bool MANY, bool TAIL, bool MX>
 __global__ void __launch_bounds__(1024, VPT * kPer<RF32> <= 8 ? 8 : 4) block_norm_kernel(BlockNorm p) {
   constexpr int N = kPer<RF32>;
   __shared__ float lds[2][16][1];
@@ -149,7 +178,7 @@ __global__ void __launch_bounds__(1024, VPT * kPer<RF32> <= 8 ? 8 : 4) block_nor
         for (int i = 0; i < N; ++i) sum[0] = fmaf(z[q][i], z[q][i], sum[0]);
       }
     }
-    if (!p.a) continue;
+    if (!MX && !p.a) continue;
     team_sum<1>(sum, lds, waves, phase);
     if (!on) continue;
     r = rms_inverse(sum[0], d, p.eps);
@@ -158,7 +187,9 @@ __global__ void __launch_bounds__(1024, VPT * kPer<RF32> <= 8 ? 8 : 4) block_nor
     for (int q = 0; q < VPT; ++q) {
 #pragma unroll
       for (int i = 0; i < N; ++i) z[q][i] *= r * w_pre[q][i];
-      store_slot<AF32, TAIL, true, N>(p.a, t * d + column(q), d - column(q), pack_slot<AF32>(z[q]));
+      const Slot<AF32, N> a = pack_slot<AF32>(z[q]);
+      if (!MX || p.a) store_slot<AF32, TAIL, true, N>(p.a, t * d + column(q), d - column(q), a);
+      if constexpr (MX) store_mx(p, t, column(q), a);
     }
   }
 }
@@ -495,8 +526,13 @@ void launch_fwd(const BlockNorm& p, hipStream_t s) {
   const TeamShape t = team_shape(p.d, RF32);
   const int64_t groups = ceil_div(p.T, t.tpb);
   with_shape<RF32>(t.vpt, p.gate && p.gate_every < p.T, p.d % kPer<RF32> != 0, [&](auto V, auto MANY, auto TAIL) {
-    block_norm_kernel<AF32, RF32, V.value, MANY.value, TAIL.value>
-        <<<dim3((unsigned)(groups < kGroups ? groups : kGroups)), dim3(t.th, t.tpb), 0, s>>>(p);
+    auto go = [&](auto kernel) {
+      kernel<<<dim3((unsigned)(groups < kGroups ? groups : kGroups)), dim3(t.th, t.tpb), 0, s>>>(p);
+    };
+    if constexpr (!AF32 && !TAIL.value) {
+      if (p.a_q) return go(block_norm_kernel<AF32, RF32, V.value, MANY.value, false, true>);
+    }
+    go(block_norm_kernel<AF32, RF32, V.value, MANY.value, TAIL.value, false>);
   });
 }
 

@@ -244,6 +244,9 @@ hipError_t launch_fill_zero(void* p, size_t bytes, hipStream_t s);
 hipError_t launch_combine(bool act_f32, const void* o_perm, const int32_t* token_row, const float* topk_w,
                           const void* y_shared, void* y, int64_t T, int d, int k, hipStream_t s);
 
+// moe_workspace_bytes, which = 6 (api_mxfp4.cpp).
+moe_status routed_ffn_workspace_bytes(const moe_dims* dims, size_t* bytes);
+
 // moe_workspace_bytes, which = 5 (api_block.cpp).
 moe_status sort_workspace_bytes(const moe_dims* dims, moe_prec prec, size_t* bytes);
 
@@ -253,6 +256,10 @@ size_t sort_scratch_bytes(int64_t T, int k, int E);
 hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k,
                        int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm,
                        void* scratch, hipStream_t s);
+// Rows of d E4M3 codes with d / 32 scale bytes each (d a multiple of 32).
+hipError_t launch_sort_mx(const int32_t* topk_idx, const uint8_t* x, const uint8_t* x_scale, int64_t T, int d, int E,
+                          int k, int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row,
+                          uint8_t* x_perm, uint8_t* x_perm_scale, void* scratch, hipStream_t s);
 hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, const float* w, const void* add, void* y,
                          int64_t T, int d, int k, hipStream_t s);
 hipError_t launch_unsort_bwd(bool f32, const void* dy, const void* o_perm, const int32_t* token_row, const float* w,

@@ -235,17 +235,46 @@ RowShape row_shape(bool f32, int64_t T, int d, int most = 1024) {
   return {dim3((unsigned)ceil_div(T, tok)), dim3((unsigned)th, (unsigned)tok)};
 }
 
+// Scale rows of MX tokens, n bytes each: read and written as words where the
+// rows are whole words (d a multiple of 128), else as bytes.
+struct ScaleRows {
+  const uint8_t* from;
+  uint8_t* to;
+  int n;
+};
+// The token's scale bytes go to the rows row(0), ..., row(k - 1) that are there.
+template <class Row>
+__device__ __forceinline__ void copy_scales(const ScaleRows& s, int64_t t, int k, Row row) {
+  auto copy = [&](auto unit) {
+    typedef decltype(unit) W;
+    const int n = s.n / (int)sizeof(W);
+    const W* from = reinterpret_cast<const W*>(s.from) + t * n;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const W v = from[i];
+      for (int j = 0; j < k; ++j) {
+        const int64_t r = row(j);
+        if (r >= 0) reinterpret_cast<W*>(s.to)[r * n + i] = v;
+      }
+    }
+  };
+  if (s.n % 4 == 0)
+    copy(uint32_t());
+  else
+    copy(uint8_t());
+}
+
 // The whole sort in one launch for a few routes, at the cost of every
 // workgroup reading all the ids: workgroup t < T finds the rows of token t's
 // routes by counting the routes that come before them (an expert below, or
 // the same expert and a smaller route) and copies the token; workgroup T
 // makes the counts and offsets.  At least 256 threads.
-template <bool F32, bool TAIL>
+template <bool F32, bool TAIL, bool MX>
 __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restrict__ idx, const void* __restrict__ x,
                                                         int T, int d, int E, int k, int32_t* __restrict__ counts,
                                                         int32_t* __restrict__ offsets,
                                                         int32_t* __restrict__ row_token,
-                                                        int32_t* __restrict__ token_row, void* __restrict__ xp) {
+                                                        int32_t* __restrict__ token_row, void* __restrict__ xp,
+                                                        ScaleRows scales) {
   __shared__ int32_t h[1024];
   __shared__ int32_t part[16][16];
   __shared__ int lds[16];
@@ -312,6 +341,7 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
   }
   if (!xp) return;
   __syncthreads();
+  if constexpr (MX) copy_scales(scales, t, k, [&](int j) { return h[j]; });
   while (c < d) {
     for (int j = 0; j < k; ++j) {
       const int row = __builtin_amdgcn_readfirstlane(h[j]);
@@ -324,12 +354,18 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
 
 constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
 
-template <bool F32, bool TAIL>
+template <bool F32, bool TAIL, bool MX>
 __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
                                                          const int32_t* __restrict__ token_row, void* __restrict__ xp,
-                                                         int64_t T, int k, int d) {
+                                                         int64_t T, int k, int d, ScaleRows scales) {
   const int64_t t = uniform_i64((int64_t)blockIdx.x * blockDim.y + threadIdx.y);
   if (t >= T) return;
+  if constexpr (MX) {
+    copy_scales(scales, t, k, [&](int j) {
+      const int64_t row = token_row[t * k + j];
+      return row_here(row, T * k) ? row : -1;
+    });
+  }
   for (int c = threadIdx.x * kPer<F32>; c < d; c += blockDim.x * kPer<F32>) {
     const Slot16<F32> s = load16<F32, TAIL>(x, t * d + c, d - c);
     for (int j = 0; j < k; ++j) {
@@ -500,9 +536,11 @@ size_t sort_scratch_bytes(int64_t T, int k, int E) {
   return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
 }
 
-hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k,
-                       int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm,
-                       void* scratch, hipStream_t s) {
+namespace {
+
+hipError_t sort_rows(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k, int32_t* counts,
+                     int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm, const ScaleRows& scales,
+                     void* scratch, hipStream_t s) {
   if (T == 0) {
     sort_empty_kernel<<<1, 256, 0, s>>>(counts, offsets, E);
     return hipGetLastError();
@@ -511,10 +549,12 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
   if (R <= kFewRoutes) {
     const int slots = (int)ceil_div(d, f32 ? 4 : 8);
     const int th = slots <= 256 ? 256 : slots >= 1024 ? 1024 : (slots + 63) / 64 * 64;
-    const auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
-      return sort_few_kernel<F32.value, TAIL.value>;
+    auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
+      return sort_few_kernel<F32.value, TAIL.value, false>;
     });
-    kernel<<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm);
+    if (scales.n) kernel = sort_few_kernel<false, false, true>;
+    kernel<<<(unsigned)T + 1, th, 0, s>>>(topk_idx, x, (int)T, d, E, k, counts, offsets, row_token, token_row, x_perm,
+                                          scales);
     return hipGetLastError();
   }
   if (R <= kWideLimit) {
@@ -531,12 +571,30 @@ hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t
     const RowShape g = row_shape(f32, T, d, 512);  // 8,192 x 7,168, k = 8: 183 us; with up to 1,024 threads 187
     // Streaming the writes gains nothing here (8,192 x 7,168, k = 8: 196 to 197
     // us either way) and costs up to 10% where the rows fit the last cache level.
-    const auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
-      return sort_rows_kernel<F32.value, TAIL.value>;
+    auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
+      return sort_rows_kernel<F32.value, TAIL.value, false>;
     });
-    kernel<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d);
+    if (scales.n) kernel = sort_rows_kernel<false, false, true>;
+    kernel<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d, scales);
   }
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_sort(bool f32, const int32_t* topk_idx, const void* x, int64_t T, int d, int E, int k,
+                       int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row, void* x_perm,
+                       void* scratch, hipStream_t s) {
+  return sort_rows(f32, topk_idx, x, T, d, E, k, counts, offsets, row_token, token_row, x_perm, ScaleRows{}, scratch,
+                   s);
+}
+
+// A row of d codes is copied as d / 2 elements of two bytes.
+hipError_t launch_sort_mx(const int32_t* topk_idx, const uint8_t* x, const uint8_t* x_scale, int64_t T, int d, int E,
+                          int k, int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_row,
+                          uint8_t* x_perm, uint8_t* x_perm_scale, void* scratch, hipStream_t s) {
+  return sort_rows(false, topk_idx, x, T, d / 2, E, k, counts, offsets, row_token, token_row, x_perm,
+                   ScaleRows{x_scale, x_perm_scale, d / 32}, scratch, s);
 }
 
 hipError_t launch_unsort(bool f32, const void* rows, const int32_t* token_row, const float* w, const void* add, void* y,
