@@ -577,8 +577,10 @@ typedef struct {
  * route, another rank's expert) adds nothing, whatever its weight holds; a
  * token without routes gives y_add or zeros.  An id may come more than once.
  * A token's result does not depend on the others of its batch.
- * Only T, d, E, k and I of dims are read: d and I multiples of 128, I * d below
- * 2^32, T <= 4,194,303, 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E).  Any T
+ * Only T, d, E, k and I of dims are read: d and I multiples of 128; T * d and
+ * T * k * I below 2^31, I * d and E * I * d / 32 below 2^32, T <= 4,194,303 (else
+ * MOE_EUNSUPPORTED);
+ * 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E).  Any T
  * is computed; from some hundred routes an expert on moe_expert_ffn is
  * faster.  ws: moe_workspace_bytes(which = 6) bytes. */
 moe_status moe_routed_ffn_mxfp4(const moe_dims* dims, const uint8_t* x, const uint8_t* x_scale,

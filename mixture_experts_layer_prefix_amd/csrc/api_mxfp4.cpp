@@ -16,11 +16,14 @@ moe_status check_matrix(int64_t rows, int64_t cols) {
   return rows > kMaxRows || cols > kMaxCols ? MOE_EUNSUPPORTED : MOE_OK;
 }
 
-// I_shared and n_shared are not read.  A byte offset inside an expert's codes
-// fits in 31 bits.
+// I_shared and n_shared are not read.  Byte offsets inside the tokens, h, an
+// expert's codes and all experts' scales fit in 31 or 32 bits.
 moe_status check_ffn(const moe_dims* D) {
   if (!D || D->T < 0 || D->d < 1 || D->I < 1 || D->E < 1 || D->E > 1024 || D->k < 1 || D->k > 16) return MOE_EINVAL;
-  if (D->T > kMaxTokens || D->d % 128 || D->I % 128 || (int64_t)D->I * D->d > UINT32_MAX) return MOE_EUNSUPPORTED;
+  if (D->T > kMaxTokens || D->d % 128 || D->I % 128 || (int64_t)D->I * D->d > UINT32_MAX ||
+      D->T * D->d > INT32_MAX || D->T * D->k > INT32_MAX / D->I ||
+      (int64_t)D->E * D->I > (int64_t)32 * UINT32_MAX / D->d)
+    return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 

@@ -43,16 +43,17 @@ __device__ __forceinline__ float silu_f32(float z) { return z * sigmoid_f32(z); 
 // writes 64 * BYTES contiguous bytes starting at lds_dst.  Only whole-dword
 // transfers are allowed: a 1- or 2-byte transfer still writes a full dword
 // per lane, which overruns the destination (it once corrupted the group
-// tables behind a slab ring).  The destination must be BYTES-aligned.
+// tables behind a slab ring).  The destination must be BYTES-aligned.  AUX: 0,
+// or 2 for the streaming hint.
 typedef __attribute__((address_space(3))) void lds_void_t;
-template <int BYTES>
+template <int BYTES, int AUX = 0>
 __device__ __forceinline__ void lds_dma(__amdgpu_buffer_rsrc_t rsrc, void* lds_dst, uint32_t voffset,
                                         uint32_t soffset) {
   static_assert(BYTES == 4 || BYTES == 16, "LDS-DMA transfers whole dwords: 4 or 16 bytes per lane");
   if constexpr (BYTES == 16)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 16, voffset, soffset, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 16, voffset, soffset, 0, AUX);
   else
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 4, voffset, soffset, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void_t*)lds_dst, 4, voffset, soffset, 0, AUX);
 }
 
 // Reductions over the 32 lanes of each wave half (lanes 0-31 and 32-63) with

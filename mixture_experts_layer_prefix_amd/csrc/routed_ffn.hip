@@ -16,7 +16,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;      // of a workgroup, which share the K of a tile
+constexpr int kDirect = 1024;  // routes up to which a workgroup finds its expert's tokens by itself
+
+// The wave's number in its workgroup, in a scalar register.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Lane l = 16 g + r of the operation feeds weight row r with K[32g, 32g+32)
 // and its scale, and token r with K[16g, 16g+16), K[64+16g, 64+16g+16) and the
@@ -28,129 +32,447 @@ __device__ __forceinline__ f32x4 mma(u32x4 w, uint32_t ws, u32x4 lo, u32x4 hi, u
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, (int)ws, 0, (int)xs);
 }
 
-struct Tile {
-  const uint8_t* codes;   // the lane's codes in slab 0
-  const uint8_t* scale;   // the scale word of the lane's row in slab 0
+// Bytes that are read through a buffer address: reads at or past the end (the
+// sum of a scalar and a lane's offset) give zeros and cost no traffic.
+struct Bytes {
+  const uint8_t* p;
+  uint32_t n;
+  __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc() const {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, (int)n, 0x00027000);
+  }
 };
 
-// NT tiles of sixteen rows of a chunk of an expert's tokens.
-template <int NT>
-__global__ void __launch_bounds__(256) gate_up_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
-                                                      const int32_t* __restrict__ row_token,
-                                                      uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
-  __shared__ f32x4 part[kWaves][4 * NT][64];
-  const int e = blockIdx.y, c0 = blockIdx.x * 32;
-  const int first = offsets[e], end = offsets[e + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const int slabs = p.d / 128;
-  const int64_t ld = p.d / 2, step = (int64_t)p.E * p.I * 4;
-  const uint8_t *wq[4], *ws[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int64_t row = (int64_t)e * p.I + c0 + (m & 1) * 16 + r;
-    wq[m] = (m < 2 ? p.w.q_gate : p.w.q_up) + row * ld + 16 * g;
-    ws[m] = (m < 2 ? p.w.q_gate_scale : p.w.q_up_scale) + row * 4;
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Loads before are issued before, loads behind behind: waits count them.
+__device__ __forceinline__ void in_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's ring in LDS for 16 * TILES weight rows, a stage for each pair of
+// slabs (256 of K).  Codes: direct loads to LDS of eight rows' whole 128-byte
+// lines, which the streaming hint needs (1.6 GB read so reach 7.0 TB/s, without
+// the hint 6.3; as sixteen rows of half a line with the hint 5.0), and which
+// hold no registers while they are under way.  A lane's 16 bytes are put in a
+// place turned by its row, so that the reads of sixteen rows of a slab meet no
+// bank twice.  Scales: a word per row and slab.
+template <int TILES, int STAGES>
+struct Ring {
+  static constexpr int kCodes = TILES * 2048, kScales = TILES * 128, kStage = kCodes + kScales;
+  static constexpr int kMats = TILES >= 2 ? 2 : 1;                    // halves of the rows, from a matrix each
+  static constexpr int kRows = 16 * TILES / kMats;                    // of a half
+  static constexpr int kScaleLoads = kRows > 32 ? kRows / 32 : 1;     // of a half: 64 words each
+  static constexpr int kLoads = TILES * 2 + kMats * kScaleLoads;      // of a stage
+  static_assert(kRows <= 64, "a scale load takes whole slabs");
+  uint8_t* lds;                    // the wave's ring
+  Bytes w[kMats], ws[kMats];       // the halves' codes, scales from their first rows on
+  uint32_t even, odd, scale;       // a lane's offsets in eight rows' codes, and in the scales
+  uint32_t ld, ws_step;            // bytes of eight rows' codes, between slabs of scales
+  uint32_t read, read_scale;       // a lane's place in a stage
+  int pairs;
+
+  __device__ __forceinline__ void begin(uint8_t* ring, int K, int64_t all_rows) {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    lds = ring;
+    pairs = (K + 255) / 256;
+    ld = 4 * K;
+    ws_step = (uint32_t)all_rows * 4;
+    even = (lane >> 3) * (K / 2) + ((lane & 7) ^ g) * 16;
+    odd = (lane >> 3) * (K / 2) + ((lane & 7) ^ (g + 4)) * 16;
+    scale = lane % kRows * 4 + lane / kRows * ws_step;
+    read = r * 128 + (g ^ (r >> 1)) * 16;
+    read_scale = kCodes + r * 4 + g;
   }
-  for (int n0 = first; n0 < end; n0 += 16 * NT) {
-    const uint8_t *xq[NT], *xs[NT];
+  // Half i begins at row `row` of the stacked matrix [all rows][K].
+  __device__ __forceinline__ void rows(int i, const uint8_t* codes, const uint8_t* scales, int64_t row, int K) {
+    w[i] = {codes + row * (K / 2), (uint32_t)kRows * (K / 2)};
+    ws[i] = {scales + row * 4, ws_step * (K / 128) - (uint32_t)row * 4};
+  }
+  // Starts the loads of pair i into its stage; past the last pair they read nothing.
+  __device__ __forceinline__ void issue(int i, int stage) const {
+    uint8_t* to = lds + stage * kStage;
+#pragma unroll
+    for (int j = 0; j < 2 * TILES; ++j) {
+      const int m = j / (2 * TILES / kMats), q = j % (2 * TILES / kMats);
+      lds_dma<16, 2>(w[m].rsrc(), to + j * 1024, j & 1 ? odd : even, i < pairs ? i * 128 + q * ld : w[m].n);
+    }
+    if (2 * kRows < 64 && (threadIdx.x & 63) >= 2 * kRows) return;
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+      for (int v = 0; v < kScaleLoads; ++v)
+        lds_dma<4>(ws[m].rsrc(), to + kCodes + (m * kScaleLoads + v) * 256, scale,
+                   i < pairs ? (2 * i + v) * ws_step : ws[m].n);
+  }
+  // Tile m's operand and scale of the stage's slab u.
+  __device__ __forceinline__ u32x4 codes(int stage, int m, int u) const {
+    return *reinterpret_cast<const u32x4*>(lds + stage * kStage + m * 2048 + (read ^ (u * 64)));
+  }
+  __device__ __forceinline__ uint32_t scales(int stage, int m, int u) const {
+    const int half = m / (TILES / kMats), q = m % (TILES / kMats);
+    return lds[stage * kStage + half * (kRows * 8) + u * (kRows * 4) + q * 64 + read_scale];
+  }
+};
+
+// Sixteen tokens' part of a pair of slabs, as loaded.
+struct TokenPair {
+  u32x4 lo[2], hi[2];
+  u32x2 xs;  // a word for each slab
+};
+
+// Tokens [][K] in E4M3 and their scales.
+struct Tokens {
+  Bytes x, xs;
+  int K;
+  __device__ __forceinline__ uint32_t offset(bool on, uint32_t row) const {
+    return on ? row * K + ((threadIdx.x & 63) >> 4) * 16 : x.n;
+  }
+  __device__ __forceinline__ uint32_t scale_offset(bool on, uint32_t row) const {
+    return on ? row * (K / 32) : xs.n;
+  }
+  // Pair i; the second slab of an odd last pair is not used.
+  __device__ __forceinline__ void load(int i, uint32_t o, uint32_t so, TokenPair& t) const {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      t.lo[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o, i * 256 + u * 128, 0);
+      t.hi[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o + 64, i * 256 + u * 128, 0);
+    }
+    t.xs = __builtin_amdgcn_raw_buffer_load_b64(xs.rsrc(), so, i * 8, 0);
+  }
+};
+
+// LDS of a workgroup: the waves' rings of one stage, and after a tile's product
+// its sums; and the routes of a DIRECT workgroup.  One object, whatever it
+// holds: between several the compiler tells the loads to LDS apart and waits
+// for all of them before each read.
+template <int TILES, int NT, bool DIRECT>
+struct Shared {
+  typedef Ring<TILES, 1> R;
+  static constexpr int kPart = 1024 * TILES * NT, kWave = R::kStage > kPart ? R::kStage : kPart;
+  int32_t list[DIRECT ? kDirect : 1], found[DIRECT ? kDirect / 256 : 1][kWaves];
+  uint8_t bytes[kWaves * kWave] __attribute__((aligned(16)));
+
+  __device__ __forceinline__ uint8_t* wave(int w) { return bytes + w * kWave; }
+
+  // The routes of expert e, in order, into `list`; id: the thread's ids of the
+  // routes threadIdx.x, 256 + threadIdx.x, ...  Their number, or 0 if one comes
+  // before route `mine`.
+  __device__ __forceinline__ int find(const int32_t (&id)[kDirect / 256], int e, int mine) {
+    const int lane = threadIdx.x & 63, wave = wave_id();
+    uint64_t m[kDirect / 256];
+#pragma unroll
+    for (int q = 0; q < kDirect / 256; ++q) {
+      m[q] = __ballot(id[q] == e);
+      const bool early = __any(id[q] == e && q * 256 + (int)threadIdx.x < mine);
+      if (lane == 0) found[q][wave] = early ? -65536 : __popcll(m[q]);
+    }
+    __syncthreads();
+    int count = 0;
+    bool early = false;
+#pragma unroll
+    for (int q = 0; q < kDirect / 256; ++q) {
+      for (int w = 0; w < kWaves; ++w) {
+        const int n = found[q][w];
+        early |= n < 0;
+        if (w == wave && !early && ((m[q] >> lane) & 1))
+          list[count + __popcll(m[q] & ((1ull << lane) - 1))] = q * 256 + (int)threadIdx.x;
+        count += n;
+      }
+    }
+    __syncthreads();
+    return early ? 0 : count;
+  }
+
+  // acc[m][n] += the slab pairs first, first + kWaves, ... of 16 * TILES rows
+  // and the first `tiles` (up to NT) times sixteen tokens; the first pair's
+  // weights are under way.  No barrier: the ring is the wave's own.  One pair
+  // of each wave is in flight: 8.5 or 17 KB, 139 KB on a compute unit with the
+  // sixteen or eight waves that fit.  Two stages of half as many waves: 8.5 KB
+  // stages 422 us where one takes 414 (16 tokens, 256 experts of 7,168 x 2,048).
+  __device__ __forceinline__ void product(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
+                                          const uint32_t (&xso)[NT], int first, int tiles,
+                                          f32x4 (&acc)[TILES][NT]) const {
+    const bool odd = (x.K / 128) & 1;
+    const int shift = (threadIdx.x & 63) >> 4 << 3;  // of the lane's scale in a word
+    TokenPair t[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < tiles) x.load(first, xo[n], xso[n], t[n]);
+    for (int i = first; i < ring.pairs; i += kWaves) {
+      in_order();
+      wait_loads<0>();
+      in_order();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (u == 1 && odd && i + 1 == ring.pairs) break;
+#pragma unroll
+        for (int m = 0; m < TILES; ++m) {
+          const u32x4 w = ring.codes(0, m, u);
+          const uint32_t ws = ring.scales(0, m, u);
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            if (n < tiles) acc[m][n] = mma(w, ws, t[n].lo[u], t[n].hi[u], t[n].xs[u] >> shift, acc[m][n]);
+        }
+      }
+      in_order();
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        if (n < tiles) x.load(i + kWaves, xo[n], xso[n], t[n]);
+      ring.issue(i + kWaves, 0);
+    }
+    in_order();
+    wait_loads<0>();  // the ring is free again
+    in_order();
+  }
+  // [rows' tile, tokens' tile][4 rows, token]
+  __device__ __forceinline__ void put(int w, const f32x4 (&acc)[TILES][NT]) {
+    f32x4* to = reinterpret_cast<f32x4*>(wave(w)) + (threadIdx.x & 63);
+#pragma unroll
+    for (int m = 0; m < TILES; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) to[(m * NT + n) * 64] = acc[m][n];
+  }
+  // Rows 4 j to 4 j + 3 of the tile for token r of tokens' tile n, the waves' sums in order.
+  __device__ __forceinline__ f32x4 get(int n, int j, int r) {
+    f32x4 v = {};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      v += reinterpret_cast<const f32x4*>(wave(w))[((j / 4) * NT + n) * 64 + (j % 4) * 16 + r];
+    return v;
+  }
+};
+
+// Which rows of a matrix a tile kernel's workgroup serves.  DIRECT: workgroup
+// (., i) serves the expert of route i if no earlier route has it, and finds the
+// others by reading all ids; h and o have a row per route.  Else workgroup
+// (., e) serves expert e after the sort's schedule, whose rows h and o have.
+template <bool DIRECT>
+struct Served {
+  int e, first, count;
+  int32_t id[kDirect / 256];
+
+  // False: there is nothing to do.
+  __device__ __forceinline__ bool begin(const RoutedFfn& p, const int32_t* offsets) {
+    if constexpr (DIRECT) {
+      e = p.topk_idx[blockIdx.y];
+      first = 0;
+      if ((unsigned)e >= (unsigned)p.E) return false;
+#pragma unroll
+      for (int q = 0; q < kDirect / 256; ++q) {
+        const int i = q * 256 + (int)threadIdx.x;
+        id[q] = i < (int)p.T * p.k ? p.topk_idx[i] : -1;
+      }
+      in_order();  // waited for behind the first weights, these would wait for them too
+      return true;
+    } else {
+      e = blockIdx.y;
+      first = offsets[e];
+      count = offsets[e + 1] - first;
+      return count > 0;
+    }
+  }
+  template <class S>
+  __device__ __forceinline__ bool find(S& shared) {
+    if constexpr (DIRECT) {
+      count = shared.find(id, e, blockIdx.y);
+      if (count == 0) wait_loads<0>();  // no load may reach LDS that is another workgroup's by then
+    }
+    return count > 0;
+  }
+  template <class S>
+  __device__ __forceinline__ int row(const S& shared, int i) const {
+    return DIRECT ? shared.list[i] : first + i;
+  }
+};
+
+// 8 * TILES columns of h for an expert's tokens.
+template <int TILES, int NT, bool DIRECT>
+__global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
+                                                         const int32_t* __restrict__ row_token,
+                                                         uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
+  __shared__ Shared<TILES, NT, DIRECT> shared;
+  constexpr int kCols = 8 * TILES;
+  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, c0 = blockIdx.x * kCols;
+  Served<DIRECT> my;
+  if (!my.begin(p, offsets)) return;
+  Ring<TILES, 1> ring;
+  ring.begin(shared.wave(wave), p.d, (int64_t)p.E * p.I);
+  ring.rows(0, p.w.q_gate, p.w.q_gate_scale, (int64_t)my.e * p.I + c0, p.d);
+  ring.rows(1, p.w.q_up, p.w.q_up_scale, (int64_t)my.e * p.I + c0, p.d);
+  ring.issue(wave, 0);  // the first weights are under way while the tokens are found
+  if (!my.find(shared)) return;
+  const Tokens x{{p.x, (uint32_t)(p.T * p.d)}, {p.x_scale, (uint32_t)(p.T * (p.d / 32))}, p.d};
+  for (int n0 = 0; n0 < my.count; n0 += 16 * NT) {
+    if (n0 > 0) ring.issue(wave, 0);
+    uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int row = n0 + 16 * n + r;
-      const int64_t t = row_token[row < end ? row : n0];
-      xq[n] = p.x + t * p.d + 16 * g;
-      xs[n] = p.x_scale + t * (p.d / 32) + g;
+      const int i = n0 + 16 * n + r;
+      const bool on = i < my.count;
+      const int row = on ? my.row(shared, i) : 0;
+      const uint32_t t = !on ? 0 : DIRECT ? row / p.k : row_token[row];
+      xo[n] = x.offset(on, t);
+      xso[n] = x.scale_offset(on, t);
     }
-    f32x4 acc[4][NT] = {};
-    for (int s = wave; s < slabs; s += kWaves) {
-      u32x4 w[4];
-      uint32_t sc[4];
-#pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        w[m] = *reinterpret_cast<const u32x4*>(wq[m] + s * 64);
-        sc[m] = *reinterpret_cast<const uint32_t*>(ws[m] + s * step) >> (8 * g);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4 lo = *reinterpret_cast<const u32x4*>(xq[n] + s * 128);
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(xq[n] + s * 128 + 64);
-        const uint32_t xsc = xs[n][s * 4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) acc[m][n] = mma(w[m], sc[m], lo, hi, xsc, acc[m][n]);
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int n = 0; n < NT; ++n) part[wave][n * 4 + m][lane] = acc[m][n];
+    f32x4 acc[TILES][NT] = {};
+    shared.product(ring, x, xo, xso, wave, (my.count - n0 + 15) / 16, acc);
+    shared.put(wave, acc);
     __syncthreads();
-    for (int n = wave; n < NT; n += kWaves) {
-      f32x4 v[4] = {};
-      for (int q = 0; q < kWaves; ++q)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) v[m] += part[q][n * 4 + m][lane];
-      float z[8];
+    // eight lanes per token and 32 columns, four columns each
+    for (int q = threadIdx.x >> 3; q < 16 * NT * (kCols / 32); q += 32) {
+      const int token = q % (16 * NT), j = q / (16 * NT) * 8 + (lane & 7), i = n0 + token;
+      const f32x4 gate = shared.get(token >> 4, j, token & 15);
+      const f32x4 up = shared.get(token >> 4, kCols / 4 + j, token & 15);
+      float z[4];
       uint32_t mx = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        z[i] = silu_f32(v[i / 4][i % 4]) * v[2 + i / 4][i % 4];
-        mx = max(mx, __float_as_uint(z[i]) & 0x7FFFFFFFu);
+      for (int v = 0; v < 4; ++v) {
+        z[v] = silu_f32(gate[v]) * up[v];
+        mx = max(mx, __float_as_uint(z[v]) & 0x7FFFFFFFu);
       }
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 16));
-      mx = max(mx, (uint32_t)__shfl_xor((int)mx, 32));
+      mx = max(mx, dpp_u32<0xB1>(mx));   // lane ^ 1
+      mx = max(mx, dpp_u32<0x4E>(mx));   // lane ^ 2
+      mx = max(mx, dpp_u32<0x141>(mx));  // the other four of eight lanes
       const int be = mx_block_exp_bits(mx);
       const float inv = mx_inv_scale(be);
-      const int64_t row = n0 + 16 * n + r;
-      if (row < end) {
-        uint8_t* out = h + row * p.I + c0 + 4 * g;
-        *reinterpret_cast<uint32_t*>(out) = e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
-        *reinterpret_cast<uint32_t*>(out + 16) = e4m3x4_rne_sat(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv);
-        if (g == 0) h_scale[row * (p.I / 32) + c0 / 32] = (uint8_t)(be + 127);
+      if (i < my.count) {
+        const int64_t row = my.row(shared, i);
+        *reinterpret_cast<uint32_t*>(h + row * p.I + c0 + 4 * j) =
+            e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
+        if (j % 8 == 0) h_scale[row * (p.I / 32) + (c0 + 4 * j) / 32] = (uint8_t)(be + 127);
       }
     }
     __syncthreads();
   }
 }
 
-// Each wave takes sixteen rows of the down projection and all of K.
-template <int NT>
-__global__ void __launch_bounds__(256) down_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
-                                                   const uint8_t* __restrict__ h, const uint8_t* __restrict__ h_scale,
-                                                   float* __restrict__ o) {
-  const int e = blockIdx.y, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-  const int c0 = (blockIdx.x * kWaves + (threadIdx.x >> 6)) * 16;
-  const int first = offsets[e], end = offsets[e + 1], slabs = p.I / 128;
-  const int64_t wrow = (int64_t)e * p.d + c0 + r, step = (int64_t)p.E * p.d * 4;
-  const uint8_t* wq = p.w.q_down + wrow * (p.I / 2) + 16 * g;
-  const uint8_t* ws = p.w.q_down_scale + wrow * 4;
-  for (int n0 = first; n0 < end; n0 += 16 * NT) {
-    const uint8_t *xq[NT], *xs[NT];
+// 16 * TILES columns of o for an expert's tokens.
+template <int TILES, int NT, bool DIRECT>
+__global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
+                                                      const uint8_t* h, const uint8_t* h_scale,
+                                                      float* __restrict__ o) {
+  __shared__ Shared<TILES, NT, DIRECT> shared;
+  constexpr int kCols = 16 * TILES;
+  const int wave = wave_id(), r = threadIdx.x & 15, c0 = blockIdx.x * kCols;
+  Served<DIRECT> my;
+  if (!my.begin(p, offsets)) return;
+  Ring<TILES, 1> ring;
+  ring.begin(shared.wave(wave), p.I, (int64_t)p.E * p.d);
+  ring.rows(0, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0, p.I);
+  ring.rows(1, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0 + kCols / 2, p.I);
+  ring.issue(wave, 0);
+  if (!my.find(shared)) return;
+  const Tokens x{{h, (uint32_t)(p.T * p.k * p.I)}, {h_scale, (uint32_t)(p.T * p.k * (p.I / 32))}, p.I};
+  for (int n0 = 0; n0 < my.count; n0 += 16 * NT) {
+    if (n0 > 0) ring.issue(wave, 0);
+    uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int64_t row = min(n0 + 16 * n + r, end - 1);
-      xq[n] = h + row * p.I + 16 * g;
-      xs[n] = h_scale + row * (p.I / 32) + g;
+      const int i = n0 + 16 * n + r;
+      const bool on = i < my.count;
+      const uint32_t row = on ? my.row(shared, i) : 0;
+      xo[n] = x.offset(on, row);
+      xso[n] = x.scale_offset(on, row);
     }
-    f32x4 acc[NT] = {};
-#pragma unroll 4
-    for (int s = 0; s < slabs; ++s) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(wq + s * 64);
-      const uint32_t sc = *reinterpret_cast<const uint32_t*>(ws + s * step) >> (8 * g);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4 lo = *reinterpret_cast<const u32x4*>(xq[n] + s * 128);
-        const u32x4 hi = *reinterpret_cast<const u32x4*>(xq[n] + s * 128 + 64);
-        acc[n] = mma(w, sc, lo, hi, xs[n][s * 4], acc[n]);
-      }
+    f32x4 acc[TILES][NT] = {};
+    shared.product(ring, x, xo, xso, wave, (my.count - n0 + 15) / 16, acc);
+    shared.put(wave, acc);
+    __syncthreads();
+    // four columns of a token each
+    for (int q = threadIdx.x; q < 16 * NT * (kCols / 4); q += 256) {
+      const int j = q % (kCols / 4), token = q / (kCols / 4), i = n0 + token;
+      if (i < my.count)
+        *reinterpret_cast<f32x4*>(o + (int64_t)my.row(shared, i) * p.d + c0 + 4 * j) =
+            shared.get(token >> 4, j, token & 15);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int64_t row = n0 + 16 * n + r;
-      if (row < end) *reinterpret_cast<f32x4*>(o + row * p.d + c0 + 4 * g) = acc[n];
-    }
+    __syncthreads();
   }
 }
 
-// y[t] = y_add[t] + sum_j w_j o[row_j] over the present routes in slot order.
+constexpr int kDownWaves = 8;
+
+// A token's sixteen columns of y, h with a row per route: each wave takes the
+// routes wave, wave + waves, ... with all of K, and the weighted sum runs over
+// the routes in slot order.  Sums are made as in down_kernel, in kWaves chains
+// of slab pairs, so that a token's bits do not depend on which of the two it
+// went through.  Workgroups are numbered so that an XCD takes neighbouring
+// columns, whose scales share lines, and all tokens of the same columns one
+// after another: an expert that several of them chose is read into its L2 once.
+__global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFfn p, const uint8_t* h,
+                                                                        const uint8_t* h_scale) {
+  typedef Ring<1, kWaves> R;
+  // a stage of the token: 256 bytes of h, 8 scales
+  constexpr int kRing = kWaves * R::kStage, kToken = 272;
+  __shared__ struct {
+    uint8_t rings[kDownWaves][kRing + kWaves * kToken] __attribute__((aligned(16)));
+    float part[16][16];
+  } shared;
+  const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x >> 6, r = lane & 15, g = lane >> 4;
+  const int T = (int)p.T, xcd = blockIdx.x % 8, i = blockIdx.x / 8;
+  const int t = i % T, c0 = (xcd * (p.d / 128) + i / T) * 16;
+  const bool odd = (p.I / 128) & 1;
+  uint8_t* lds = shared.rings[wave];
+  R ring;
+  ring.begin(lds, p.I, (int64_t)p.E * p.d);
+  for (int j = wave; j < p.k; j += waves) {
+    const int e = __builtin_amdgcn_readfirstlane(p.topk_idx[t * p.k + j]);
+    if ((unsigned)e >= (unsigned)p.E) continue;
+    ring.rows(0, p.w.q_down, p.w.q_down_scale, (int64_t)e * p.d + c0, p.I);
+    const int64_t row = t * p.k + j;
+    const Bytes x{h + row * p.I, (uint32_t)p.I}, xs{h_scale + row * (p.I / 32), (uint32_t)p.I / 32};
+    auto issue = [&](int i, int u) {
+      uint8_t* to = lds + kRing + u * kToken;
+      ring.issue(i, u);
+      if (lane < 16)
+        lds_dma<16>(x.rsrc(), to, lane * 16, i * 256);
+      if (lane < 2)
+        lds_dma<4>(xs.rsrc(), to + 256, lane * 4, i * 8);
+    };
+    f32x4 acc[kWaves] = {};
+    auto multiply = [&](int u, int slab) {
+      const uint8_t* x = lds + kRing + u * kToken + slab * 128 + 16 * g;  // the token in every column
+      acc[u] = mma(ring.codes(u, 0, slab), ring.scales(u, 0, slab), *reinterpret_cast<const u32x4*>(x),
+                   *reinterpret_cast<const u32x4*>(x + 64), lds[kRing + u * kToken + 256 + slab * 4 + g], acc[u]);
+    };
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) issue(u, u);
+    for (int q = 0; q < ring.pairs; q += kWaves) {
+#pragma unroll
+      for (int u = 0; u < kWaves; ++u) {
+        in_order();
+        wait_loads<(kWaves - 1) * (R::kLoads + 2)>();
+        in_order();
+        if (q + u < ring.pairs) multiply(u, 0);
+        if (q + u + (odd ? 1 : 0) < ring.pairs) multiply(u, 1);
+        in_order();
+        issue(q + u + kWaves, u);
+      }
+    }
+    in_order();
+    wait_loads<0>();  // the ring is free again
+    in_order();
+    f32x4 v = {};
+#pragma unroll
+    for (int u = 0; u < kWaves; ++u) v += acc[u];
+    if (r == 0) *reinterpret_cast<f32x4*>(&shared.part[j][4 * g]) = v;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int64_t at = (int64_t)t * p.d + c0 + threadIdx.x;
+    float v = 0.0f;
+    for (int j = 0; j < p.k; ++j)
+      if ((unsigned)p.topk_idx[t * p.k + j] < (unsigned)p.E) v = fmaf(p.topk_w[t * p.k + j], shared.part[j][threadIdx.x], v);
+    if (p.y_add) v += bf16_to_f32(p.y_add[at]);
+    p.y[at] = f32_to_bf16(v);
+  }
+}
+
+// y[t] = y_add[t] + sum_j w_j o[row_j] over the present routes in slot order;
+// token_row null: o has a row per route.
 __global__ void __launch_bounds__(256) weighted_sum_kernel(RoutedFfn p, const int32_t* __restrict__ token_row,
                                                            const float* __restrict__ o) {
   const int per = (p.d + 1023) / 1024;  // workgroup steps of a token
@@ -160,7 +482,11 @@ __global__ void __launch_bounds__(256) weighted_sum_kernel(RoutedFfn p, const in
     if (c >= p.d) continue;
     f32x4 acc = {};
     for (int j = 0; j < p.k; ++j) {
-      const int64_t row = token_row[t * p.k + j];
+      int64_t row = t * p.k + j;
+      if (token_row)
+        row = token_row[row];
+      else if ((unsigned)p.topk_idx[row] >= (unsigned)p.E)
+        row = -1;
       if (row < 0) continue;
       const float g = p.topk_w[t * p.k + j];
       const f32x4 v = *reinterpret_cast<const f32x4*>(o + row * p.d + c);
@@ -216,13 +542,29 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
 
 hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const Scratch b = carve(static_cast<char*>(scratch), p.T, p.d, p.E, p.k, p.I);
+  const int64_t R = p.T * p.k, steps = p.T * ceil_div(p.d, 1024);
+  const unsigned sums = (unsigned)(steps < 65536 ? steps : 65536);
+#ifndef TOK
+#define TOK 8
+#endif
+  if (R <= kDirect && R <= p.E) {
+    const unsigned routes = (unsigned)R;
+    gate_up_kernel<4, 1, true><<<dim3(p.I / 32, routes), 256, 0, s>>>(p, nullptr, nullptr, b.h, b.h_scale);
+    if (p.T == 1 || R * TOK <= p.E) {
+      const int waves = p.k < kDownWaves ? p.k : kDownWaves;
+      down_token_kernel<<<(unsigned)(p.T * (p.d / 16)), 64 * waves, 0, s>>>(p, b.h, b.h_scale);
+      return hipGetLastError();
+    }
+    down_kernel<4, 1, true><<<dim3(p.d / 64, routes), 256, 0, s>>>(p, nullptr, b.h, b.h_scale, b.o);
+    weighted_sum_kernel<<<sums, 256, 0, s>>>(p, nullptr, b.o);
+    return hipGetLastError();
+  }
   const hipError_t e = launch_sort(false, p.topk_idx, nullptr, p.T, p.d, p.E, p.k, b.counts, b.offsets, b.row_token,
                                    b.token_row, nullptr, b.sort, s);
   if (e != hipSuccess) return e;
-  gate_up_kernel<1><<<dim3(p.I / 32, p.E), 256, 0, s>>>(p, b.offsets, b.row_token, b.h, b.h_scale);
-  down_kernel<1><<<dim3(p.d / 64, p.E), 256, 0, s>>>(p, b.offsets, b.h, b.h_scale, b.o);
-  const int64_t steps = p.T * ceil_div(p.d, 1024);
-  weighted_sum_kernel<<<(unsigned)(steps < 65536 ? steps : 65536), 256, 0, s>>>(p, b.token_row, b.o);
+  gate_up_kernel<8, 2, false><<<dim3(p.I / 64, p.E), 256, 0, s>>>(p, b.offsets, b.row_token, b.h, b.h_scale);
+  down_kernel<8, 2, false><<<dim3(p.d / 128, p.E), 256, 0, s>>>(p, b.offsets, b.h, b.h_scale, b.o);
+  weighted_sum_kernel<<<sums, 256, 0, s>>>(p, b.token_row, b.o);
   return hipGetLastError();
 }
 
