@@ -9,6 +9,8 @@
 // matrix cores: v_mfma_scale_f32_16x16x128_f8f6f4 takes E2M1 weights and E4M3
 // activations with their block scales as they lie in memory, sixteen weight
 // rows against sixteen tokens.
+#include <type_traits>
+
 #include "mxfp4.h"
 #include "rows.h"
 
@@ -17,7 +19,13 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;      // of a workgroup, which share the K of a tile
-constexpr int kDirect = 1024;  // routes up to which a workgroup finds its expert's tokens by itself
+// Routes up to which a workgroup finds its expert's tokens by itself, with a
+// workgroup for every route: where there are as many experts as routes, or one
+// tile holds all tokens.  It saves the schedule (8 tokens, one expert of 7,168 x
+// 2,048: 25 us, after a schedule 35; 4 tokens, 8 of 2,048 x 768, k = 4: 17, 25),
+// but reads sixteen tokens at a time (16 tokens, 8 of 4,096 x 1,536, k = 2: 36,
+// after a schedule 33).
+constexpr int kDirect = 1024;
 
 // The wave's number in its workgroup, in a scalar register.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -253,13 +261,18 @@ struct Shared {
 template <bool DIRECT>
 struct Served {
   int e, first, count;
+  int tile, part, parts;  // of the columns; of the tokens, and how many there are
   int32_t id[kDirect / 256];
 
   // False: there is nothing to do.
-  __device__ __forceinline__ bool begin(const RoutedFfn& p, const int32_t* offsets) {
+  __device__ __forceinline__ bool begin(const RoutedFfn& p, const int32_t* offsets, int tiles) {
+    tile = blockIdx.x;
+    part = 0;
+    parts = 1;
     if constexpr (DIRECT) {
       e = p.topk_idx[blockIdx.y];
       first = 0;
+      count = 1;  // at least, until find()
       if ((unsigned)e >= (unsigned)p.E) return false;
 #pragma unroll
       for (int q = 0; q < kDirect / 256; ++q) {
@@ -269,10 +282,16 @@ struct Served {
       in_order();  // waited for behind the first weights, these would wait for them too
       return true;
     } else {
+      // The parts behind the last token come last: one beside another they
+      // would leave every second compute unit without work (parts of a tile in
+      // turn: 209 us where this takes 142, 2,048 routes of which 256 are here).
       e = blockIdx.y;
+      parts = gridDim.x / tiles;
+      part = blockIdx.x / tiles;
+      tile = blockIdx.x % tiles;
       first = offsets[e];
       count = offsets[e + 1] - first;
-      return count > 0;
+      return true;
     }
   }
   template <class S>
@@ -296,9 +315,10 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
                                                          uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 8 * TILES;
-  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15, c0 = blockIdx.x * kCols;
+  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15;
   Served<DIRECT> my;
-  if (!my.begin(p, offsets)) return;
+  if (!my.begin(p, offsets, p.I / kCols) || my.part * 16 * NT >= my.count) return;
+  const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
   ring.begin(shared.wave(wave), p.d, (int64_t)p.E * p.I);
   ring.rows(0, p.w.q_gate, p.w.q_gate_scale, (int64_t)my.e * p.I + c0, p.d);
@@ -306,8 +326,8 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
   ring.issue(wave, 0);  // the first weights are under way while the tokens are found
   if (!my.find(shared)) return;
   const Tokens x{{p.x, (uint32_t)(p.T * p.d)}, {p.x_scale, (uint32_t)(p.T * (p.d / 32))}, p.d};
-  for (int n0 = 0; n0 < my.count; n0 += 16 * NT) {
-    if (n0 > 0) ring.issue(wave, 0);
+  for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
+    if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -357,9 +377,10 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
                                                       float* __restrict__ o) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 16 * TILES;
-  const int wave = wave_id(), r = threadIdx.x & 15, c0 = blockIdx.x * kCols;
+  const int wave = wave_id(), r = threadIdx.x & 15;
   Served<DIRECT> my;
-  if (!my.begin(p, offsets)) return;
+  if (!my.begin(p, offsets, p.d / kCols) || my.part * 16 * NT >= my.count) return;
+  const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
   ring.begin(shared.wave(wave), p.I, (int64_t)p.E * p.d);
   ring.rows(0, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0, p.I);
@@ -367,8 +388,8 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
   ring.issue(wave, 0);
   if (!my.find(shared)) return;
   const Tokens x{{h, (uint32_t)(p.T * p.k * p.I)}, {h_scale, (uint32_t)(p.T * p.k * (p.I / 32))}, p.I};
-  for (int n0 = 0; n0 < my.count; n0 += 16 * NT) {
-    if (n0 > 0) ring.issue(wave, 0);
+  for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
+    if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -540,17 +561,35 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
   return carve(nullptr, T, d, E, k, I).bytes;
 }
 
+// Which down projection.  By token it needs no sum of its own, which saves a
+// launch and o's way through memory, but reads an expert anew for every token
+// that chose it: R^2 / 2E of R routes at random, weighed here in weights.  us of
+// the whole call, by token and by expert (tokens, experts of d x I, k):
+//   1, 256 of 7,168 x 2,048, 8      39.2  -         5, 64 of 2,048 x 768, 6    24.2  26.0
+//   3                               95.9  97.0      8                          31.3  34.6
+//   4                               122.7 121.0     10                         38.2  37.8
+//   8                               222.3 216.2     4, 128 of 4,096 x 1,536, 8 59.3  62.4
+//   16                              413.7 392.0     8                          103.9 99.4
+constexpr int64_t kRepeats = 60000000;
+
+// Which tiles, after the schedule.  128 rows against 32 tokens read each token
+// half as often as 64 rows do (333 tokens, 128 experts of 4,096 x 1,536: 268 us,
+// 294; 300, 4 of 4,096 x 2,048, k = 2: 77, 83), 64 rows give twice the
+// workgroups where those are few (64 tokens, one expert of 7,168 x 2,048: 45,
+// 35; 16 tokens, 8 of 4,096 x 1,536: 31.5, 29.6).  An expert's tokens are
+// shared by as many workgroups as the mean calls for (512 tokens, one expert
+// of 7,168 x 2,048: 532 us with one, 87 with sixteen).
+constexpr int kTokenTiles = 2;
+constexpr int64_t kFewGroups = 512;
+
 hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const Scratch b = carve(static_cast<char*>(scratch), p.T, p.d, p.E, p.k, p.I);
   const int64_t R = p.T * p.k, steps = p.T * ceil_div(p.d, 1024);
   const unsigned sums = (unsigned)(steps < 65536 ? steps : 65536);
-#ifndef TOK
-#define TOK 8
-#endif
-  if (R <= kDirect && R <= p.E) {
+  if (R <= kDirect && (R <= p.E || R <= 16)) {
     const unsigned routes = (unsigned)R;
     gate_up_kernel<4, 1, true><<<dim3(p.I / 32, routes), 256, 0, s>>>(p, nullptr, nullptr, b.h, b.h_scale);
-    if (p.T == 1 || R * TOK <= p.E) {
+    if (p.T == 1 || R * R * p.I * p.d / p.E <= kRepeats) {
       const int waves = p.k < kDownWaves ? p.k : kDownWaves;
       down_token_kernel<<<(unsigned)(p.T * (p.d / 16)), 64 * waves, 0, s>>>(p, b.h, b.h_scale);
       return hipGetLastError();
@@ -562,8 +601,19 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const hipError_t e = launch_sort(false, p.topk_idx, nullptr, p.T, p.d, p.E, p.k, b.counts, b.offsets, b.row_token,
                                    b.token_row, nullptr, b.sort, s);
   if (e != hipSuccess) return e;
-  gate_up_kernel<8, 2, false><<<dim3(p.I / 64, p.E), 256, 0, s>>>(p, b.offsets, b.row_token, b.h, b.h_scale);
-  down_kernel<8, 2, false><<<dim3(p.d / 128, p.E), 256, 0, s>>>(p, b.offsets, b.h, b.h_scale, b.o);
+  const int64_t want = ceil_div(R, (int64_t)p.E * 16 * kTokenTiles);
+  const int parts = (int)(want < 64 ? want : 64);
+  auto tiles = [&](auto TILES) {
+    constexpr int t = TILES.value;
+    gate_up_kernel<t, kTokenTiles, false><<<dim3((unsigned)(p.I / (8 * t) * parts), (unsigned)p.E), 256, 0, s>>>(
+        p, b.offsets, b.row_token, b.h, b.h_scale);
+    down_kernel<t, kTokenTiles, false><<<dim3((unsigned)(p.d / (16 * t) * parts), (unsigned)p.E), 256, 0, s>>>(
+        p, b.offsets, b.h, b.h_scale, b.o);
+  };
+  if ((int64_t)p.E * (p.I / 64) * parts < kFewGroups)
+    tiles(std::integral_constant<int, 4>());
+  else
+    tiles(std::integral_constant<int, 8>());
   weighted_sum_kernel<<<sums, 256, 0, s>>>(p, b.token_row, b.o);
   return hipGetLastError();
 }
