@@ -9,6 +9,7 @@
 // matrix cores: v_mfma_scale_f32_16x16x128_f8f6f4 takes E2M1 weights and E4M3
 // activations with their block scales as they lie in memory, sixteen weight
 // rows against sixteen tokens.
+#include <algorithm>
 #include <type_traits>
 
 #include "mxfp4.h"
@@ -415,6 +416,10 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
 }
 
 constexpr int kDownWaves = 8;
+// Two stages let four workgroups onto a compute unit (four stages two of them,
+// with as much in flight: 4 tokens, 256 experts of 7,168 x 2,048, 123 us, with
+// two 116; 5 tokens, 64 of 2,048 x 768, 24.5, 21.7).
+constexpr int kTokenStages = 2;
 
 // A token's sixteen columns of y, h with a row per route: each wave takes the
 // routes wave, wave + waves, ... with all of K, and the weighted sum runs over
@@ -425,11 +430,11 @@ constexpr int kDownWaves = 8;
 // after another: an expert that several of them chose is read into its L2 once.
 __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFfn p, const uint8_t* h,
                                                                         const uint8_t* h_scale) {
-  typedef Ring<1, kWaves> R;
+  typedef Ring<1, kTokenStages> R;
   // a stage of the token: 256 bytes of h, 8 scales
-  constexpr int kRing = kWaves * R::kStage, kToken = 272;
+  constexpr int kRing = kTokenStages * R::kStage, kToken = 272;
   __shared__ struct {
-    uint8_t rings[kDownWaves][kRing + kWaves * kToken] __attribute__((aligned(16)));
+    uint8_t rings[kDownWaves][kRing + kTokenStages * kToken] __attribute__((aligned(16)));
     float part[16][16];
   } shared;
   const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x >> 6, r = lane & 15, g = lane >> 4;
@@ -454,23 +459,23 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
         lds_dma<4>(xs.rsrc(), to + 256, lane * 4, i * 8);
     };
     f32x4 acc[kWaves] = {};
-    auto multiply = [&](int u, int slab) {
-      const uint8_t* x = lds + kRing + u * kToken + slab * 128 + 16 * g;  // the token in every column
-      acc[u] = mma(ring.codes(u, 0, slab), ring.scales(u, 0, slab), *reinterpret_cast<const u32x4*>(x),
-                   *reinterpret_cast<const u32x4*>(x + 64), lds[kRing + u * kToken + 256 + slab * 4 + g], acc[u]);
+    auto multiply = [&](int u, int stage, int slab) {
+      const uint8_t* x = lds + kRing + stage * kToken + slab * 128 + 16 * g;  // the token in every column
+      acc[u] = mma(ring.codes(stage, 0, slab), ring.scales(stage, 0, slab), *reinterpret_cast<const u32x4*>(x),
+                   *reinterpret_cast<const u32x4*>(x + 64), lds[kRing + stage * kToken + 256 + slab * 4 + g], acc[u]);
     };
 #pragma unroll
-    for (int u = 0; u < kWaves; ++u) issue(u, u);
+    for (int u = 0; u < kTokenStages; ++u) issue(u, u);
     for (int q = 0; q < ring.pairs; q += kWaves) {
 #pragma unroll
       for (int u = 0; u < kWaves; ++u) {
         in_order();
-        wait_loads<(kWaves - 1) * (R::kLoads + 2)>();
+        wait_loads<(kTokenStages - 1) * (R::kLoads + 2)>();
         in_order();
-        if (q + u < ring.pairs) multiply(u, 0);
-        if (q + u + (odd ? 1 : 0) < ring.pairs) multiply(u, 1);
+        if (q + u < ring.pairs) multiply(u, u % kTokenStages, 0);
+        if (q + u + (odd ? 1 : 0) < ring.pairs) multiply(u, u % kTokenStages, 1);
         in_order();
-        issue(q + u + kWaves, u);
+        issue(q + u + kTokenStages, u % kTokenStages);
       }
     }
     in_order();
@@ -563,14 +568,15 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
 
 // Which down projection.  By token it needs no sum of its own, which saves a
 // launch and o's way through memory, but reads an expert anew for every token
-// that chose it: R^2 / 2E of R routes at random, weighed here in weights.  us of
-// the whole call, by token and by expert (tokens, experts of d x I, k):
-//   1, 256 of 7,168 x 2,048, 8      39.2  -         5, 64 of 2,048 x 768, 6    24.2  26.0
-//   3                               95.9  97.0      8                          31.3  34.6
-//   4                               122.7 121.0     10                         38.2  37.8
-//   8                               222.3 216.2     4, 128 of 4,096 x 1,536, 8 59.3  62.4
-//   16                              413.7 392.0     8                          103.9 99.4
-constexpr int64_t kRepeats = 60000000;
+// that chose it: R^2 / 2E experts for R routes at random, weighed here in
+// weights.  us of the whole call, by token and by expert (tokens, experts of d x
+// I, k):
+//   1, 256 of 7,168 x 2,048, 8    39.0  -        2, 64 of 2,048 x 768, 6    17.5  23.2
+//   2                             63.7  70.7     5                          21.5  26.2
+//   4                             116.0 120.9    10                         35.5  38.0
+//   8                             213.5 216.2    4, 128 of 4,096 x 1,536, 8 56.5  62.0
+//   16                            393.7 391.8    8                          97.7  99.4
+constexpr int64_t kRepeats = 500000000;
 
 // Which tiles, after the schedule.  128 rows against 32 tokens read each token
 // half as often as 64 rows do (333 tokens, 128 experts of 4,096 x 1,536: 268 us,
@@ -602,7 +608,8 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
                                    b.token_row, nullptr, b.sort, s);
   if (e != hipSuccess) return e;
   const int64_t want = ceil_div(R, (int64_t)p.E * 16 * kTokenTiles);
-  const int parts = (int)(want < 64 ? want : 64);
+  const int64_t most = (1 << 22) / (p.I / 32 + p.d / 64);  // workgroups in x: threads stay below 2^32
+  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min<int64_t>(most, 64)));
   auto tiles = [&](auto TILES) {
     constexpr int t = TILES.value;
     gate_up_kernel<t, kTokenTiles, false><<<dim3((unsigned)(p.I / (8 * t) * parts), (unsigned)p.E), 256, 0, s>>>(
