@@ -16,6 +16,13 @@ from .ops import Dims, Weights
 _U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
 
 
+def _given(name, t, dtype, shape, device):
+    """_check of a tensor that may not be missing."""
+    if t is None:
+        raise ValueError("%s is missing" % name)
+    return _check(name, t, dtype, shape, device)
+
+
 # ---- norms whose output is in 8 bits ---------------------------------------
 class BlockNormMxfp8Plan(BlockNormPlan):
     """Outputs of moe_block_norm_mxfp8 for one configuration: x_out [T][d]
@@ -37,8 +44,7 @@ class BlockNormMxfp8Plan(BlockNormPlan):
         """(x_out, a_q, a_scale); x_out is x itself where there is no block
         output y.  With keep_a the bf16 a is in self.a."""
         dev = self.device
-        _need("x", x)
-        px, py = _check("x", x, self._res, self._rows, dev), _check("y", y, self._act, self._rows, dev)
+        px, py = _given("x", x, self._res, self._rows, dev), _check("y", y, self._act, self._rows, dev)
         _launch(dev, "moe_block_norm_mxfp8", self.cblock, px, py, *self._vectors(w_pre, w_post, gate),
                 None if y is None or self.x_out is None else self.x_out.data_ptr(),
                 None if self.a is None else self.a.data_ptr(), self.a_q.data_ptr(), self.a_scale.data_ptr(),
@@ -85,10 +91,8 @@ class SortMxfp8Plan:
         """(counts, offsets, row_token, token_row, x_perm, x_perm_scale) of the
         ids topk_idx [T][k] int32 and the tokens x [T][d], x_scale [T][d/32]."""
         dev = self.device
-        for name, t in (("topk_idx", topk_idx), ("x", x), ("x_scale", x_scale)):
-            _need(name, t)
-        args = (_check("topk_idx", topk_idx, _I32, self._ids, dev), _check("x", x, _U8, self._rows, dev),
-                _check("x_scale", x_scale, _U8, self._scales, dev))
+        args = (_given("topk_idx", topk_idx, _I32, self._ids, dev), _given("x", x, _U8, self._rows, dev),
+                _given("x_scale", x_scale, _U8, self._scales, dev))
         _launch(dev, "moe_sort_tokens_mxfp8", self.cdims, *args, self.counts.data_ptr(), self.offsets.data_ptr(),
                 self.row_token.data_ptr(), self.token_row.data_ptr(), self.x_perm.data_ptr(),
                 self.x_perm_scale.data_ptr(), self.ws.data_ptr(), self.ws_bytes)
@@ -127,7 +131,7 @@ def dequantize_mxfp4(codes, scale):
             tuple(codes.shape),))
     rows, cols = codes.shape[0], 2 * codes.shape[1]
     args = (_check("codes", codes, _U8, (rows, cols // 2), dev),
-            _check("scale", scale, _U8, (cols // 128, rows, 4), _need("scale", scale) and dev))
+            _given("scale", scale, _U8, (cols // 128, rows, 4), dev))
     dst = torch.empty(rows, cols, dtype=_BF16, device=dev)
     _launch(dev, "moe_dequantize_mxfp4", *args, rows, cols, dst.data_ptr())
     return dst
@@ -181,15 +185,9 @@ class RoutedFfnPlan:
         """y [T][d] of the tokens x [T][d], x_scale [T][d/32], their ids and
         weights [T][k]; y_add [T][d] bf16 or None is added."""
         dev = self.device
-        for name, t in (("x", x), ("x_scale", x_scale), ("topk_idx", topk_idx), ("topk_w", topk_w)):
-            _need(name, t)
-        args = (_check("x", x, _U8, self._x, dev), _check("x_scale", x_scale, _U8, self._scale, dev),
-                _check("topk_idx", topk_idx, _I32, self._ids, dev), _check("topk_w", topk_w, _F32, self._ids, dev))
-        w = moe_weights_mxfp4()
-        for name, shape in self._shapes:
-            t = getattr(weights, name)
-            _need(name, t)
-            setattr(w, name, _check(name, t, _U8, shape, dev))
+        args = (_given("x", x, _U8, self._x, dev), _given("x_scale", x_scale, _U8, self._scale, dev),
+                _given("topk_idx", topk_idx, _I32, self._ids, dev), _given("topk_w", topk_w, _F32, self._ids, dev))
+        w = moe_weights_mxfp4(*[_given(name, getattr(weights, name), _U8, shape, dev) for name, shape in self._shapes])
         add = _check("y_add", y_add, _BF16, self._x, dev)
         _launch(dev, "moe_routed_ffn_mxfp4", self.cdims, *args, w, add, self.y.data_ptr(), self.ws.data_ptr(),
                 self.ws_bytes)
