@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(1024) sort_few_kernel(const int32_t* __restric
 
 constexpr int kRoutes = 8;  // routes whose rows a thread has in flight
 
-template <bool F32, bool TAIL, bool MX>
+// MX: rows of codes with their scales.  STREAM: written with the hint that they
+// are not read soon.
+template <bool F32, bool TAIL, bool MX, bool STREAM>
 __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict__ x,
                                                          const int32_t* __restrict__ token_row, void* __restrict__ xp,
                                                          int64_t T, int k, int d, ScaleRows scales) {
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(1024) sort_rows_kernel(const void* __restrict_
     const Slot16<F32> s = load16<F32, TAIL>(x, t * d + c, d - c);
     for (int j = 0; j < k; ++j) {
       const int64_t row = token_row[t * k + j];
-      if (row_here(row, T * k)) store16<F32, TAIL>(xp, row * d + c, d - c, s);
+      if (row_here(row, T * k)) store16<F32, TAIL, STREAM>(xp, row * d + c, d - c, s);
     }
   }
 }
@@ -572,9 +574,14 @@ hipError_t sort_rows(bool f32, const int32_t* topk_idx, const void* x, int64_t T
     // Streaming the writes gains nothing here (8,192 x 7,168, k = 8: 196 to 197
     // us either way) and costs up to 10% where the rows fit the last cache level.
     auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
-      return sort_rows_kernel<F32.value, TAIL.value, false>;
+      return sort_rows_kernel<F32.value, TAIL.value, false, false>;
     });
-    if (scales.n) kernel = sort_rows_kernel<false, false, true>;
+    // Codes are half as many bytes a row, and streaming them gains: 8,192 x
+    // 7,168, k = 8: 130 us, streaming 108, with a kernel that reads the rows next
+    // 281 and 284; 2,048: 37, 31 and 74, 71; 1,024: 18, 18 and 37, 38.
+    if (scales.n)
+      kernel = T * k * d * 2 > (96ll << 20) ? sort_rows_kernel<false, false, true, true>
+                                            : sort_rows_kernel<false, false, true, false>;
     kernel<<<g.grid, g.block, 0, s>>>(x, token_row, x_perm, T, k, d, scales);
   }
   return hipGetLastError();

@@ -77,7 +77,9 @@ def ffn_status(x=FAKE, xs=FAKE, idx=FAKE, w=FAKE, add=None, y=FAKE, ws=FAKE, ws_
     (dict(T=-1), L.MOE_EINVAL), (dict(d=0), L.MOE_EINVAL), (dict(I=0), L.MOE_EINVAL), (dict(E=0), L.MOE_EINVAL),
     (dict(E=1025), L.MOE_EINVAL), (dict(k=0), L.MOE_EINVAL), (dict(k=17), L.MOE_EINVAL),
     (dict(T=1 << 23), L.MOE_EUNSUPPORTED), (dict(d=192), L.MOE_EUNSUPPORTED), (dict(I=96), L.MOE_EUNSUPPORTED),
-    (dict(d=1 << 16, I=1 << 16), L.MOE_EUNSUPPORTED), (dict(x=None), L.MOE_EINVAL), (dict(x=FAKE + 8), L.MOE_EINVAL),
+    (dict(d=1 << 16, I=1 << 16), L.MOE_EUNSUPPORTED), (dict(T=1 << 20, d=2048), L.MOE_EUNSUPPORTED),
+    (dict(T=1 << 21, k=8), L.MOE_EUNSUPPORTED), (dict(E=1024, d=1 << 14, I=1 << 13), L.MOE_EUNSUPPORTED),
+    (dict(x=None), L.MOE_EINVAL), (dict(x=FAKE + 8), L.MOE_EINVAL),
     (dict(xs=None), L.MOE_EINVAL), (dict(xs=FAKE + 2), L.MOE_EINVAL), (dict(idx=None), L.MOE_EINVAL),
     (dict(w=None), L.MOE_EINVAL), (dict(add=FAKE + 8), L.MOE_EINVAL), (dict(y=None), L.MOE_EINVAL),
     (dict(weights=dict(q_up=None)), L.MOE_EINVAL), (dict(weights=dict(q_down=FAKE + 8)), L.MOE_EINVAL),
