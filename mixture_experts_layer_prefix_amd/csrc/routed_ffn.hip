@@ -161,7 +161,8 @@ struct Tokens {
 template <int TILES, int NT, bool DIRECT>
 struct Shared {
   typedef Ring<TILES, 1> R;
-  static constexpr int kPart = 1024 * TILES * NT, kWave = R::kStage > kPart ? R::kStage : kPart;
+  static constexpr int kAtOnce = TILES == 8 ? 2 : NT;  // tokens' tiles whose sums LDS holds at a time
+  static constexpr int kPart = 1024 * TILES * kAtOnce, kWave = R::kStage > kPart ? R::kStage : kPart;
   int32_t list[DIRECT ? kDirect : 1], found[DIRECT ? kDirect / 256 : 1][kWaves];
   uint8_t bytes[kWaves * kWave] __attribute__((aligned(16)));
 
@@ -237,20 +238,21 @@ struct Shared {
     wait_loads<0>();  // the ring is free again
     in_order();
   }
-  // [rows' tile, tokens' tile][4 rows, token]
-  __device__ __forceinline__ void put(int w, const f32x4 (&acc)[TILES][NT]) {
+  // [rows' tile, tokens' tile][4 rows, token] of the tokens' tiles from n0 on.
+  __device__ __forceinline__ void put(int w, int n0, const f32x4 (&acc)[TILES][NT]) {
     f32x4* to = reinterpret_cast<f32x4*>(wave(w)) + (threadIdx.x & 63);
 #pragma unroll
     for (int m = 0; m < TILES; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) to[(m * NT + n) * 64] = acc[m][n];
+      for (int n = 0; n < kAtOnce; ++n)
+        if (n0 + n < NT) to[(m * kAtOnce + n) * 64] = acc[m][n0 + n];
   }
-  // Rows 4 j to 4 j + 3 of the tile for token r of tokens' tile n, the waves' sums in order.
+  // Rows 4 j to 4 j + 3 of the tile for token r of tokens' tile n0 + n, the waves' sums in order.
   __device__ __forceinline__ f32x4 get(int n, int j, int r) {
     f32x4 v = {};
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
-      v += reinterpret_cast<const f32x4*>(wave(w))[((j / 4) * NT + n) * 64 + (j % 4) * 16 + r];
+      v += reinterpret_cast<const f32x4*>(wave(w))[((j / 4) * kAtOnce + n) * 64 + (j % 4) * 16 + r];
     return v;
   }
 };
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
                                                          const int32_t* __restrict__ row_token,
                                                          uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
-  constexpr int kCols = 8 * TILES;
+  constexpr int kCols = 8 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
   const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15;
   Served<DIRECT> my;
   if (!my.begin(p, offsets, p.I / kCols) || my.part * 16 * NT >= my.count) return;
@@ -341,33 +343,36 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
     }
     f32x4 acc[TILES][NT] = {};
     shared.product(ring, x, xo, xso, wave, (my.count - n0 + 15) / 16, acc);
-    shared.put(wave, acc);
-    __syncthreads();
-    // eight lanes per token and 32 columns, four columns each
-    for (int q = threadIdx.x >> 3; q < 16 * NT * (kCols / 32); q += 32) {
-      const int token = q % (16 * NT), j = q / (16 * NT) * 8 + (lane & 7), i = n0 + token;
-      const f32x4 gate = shared.get(token >> 4, j, token & 15);
-      const f32x4 up = shared.get(token >> 4, kCols / 4 + j, token & 15);
-      float z[4];
-      uint32_t mx = 0;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        z[v] = silu_f32(gate[v]) * up[v];
-        mx = max(mx, __float_as_uint(z[v]) & 0x7FFFFFFFu);
+    for (int n1 = 0; n1 < NT; n1 += kAtOnce) {
+      shared.put(wave, n1, acc);
+      __syncthreads();
+      // eight lanes per token and 32 columns, four columns each
+      for (int q = threadIdx.x >> 3; q < 16 * kAtOnce * (kCols / 32); q += 32) {
+        const int token = q % (16 * kAtOnce), j = q / (16 * kAtOnce) * 8 + (lane & 7), i = n0 + 16 * n1 + token;
+        const f32x4 gate = shared.get(token >> 4, j, token & 15);
+        const f32x4 up = shared.get(token >> 4, kCols / 4 + j, token & 15);
+        float z[4];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          z[v] = silu_f32(gate[v]) * up[v];
+          mx = max(mx, __float_as_uint(z[v]) & 0x7FFFFFFFu);
+        }
+        mx = max(mx, dpp_u32<0xB1>(mx));   // lane ^ 1
+        mx = max(mx, dpp_u32<0x4E>(mx));   // lane ^ 2
+        mx = max(mx, dpp_u32<0x141>(mx));  // the other four of eight lanes
+        const int be = mx_block_exp_bits(mx);
+        const float inv = mx_inv_scale(be);
+        if (i < min(my.count, n0 + 16 * NT)) {
+          const int64_t row = my.row(shared, i);
+          *reinterpret_cast<uint32_t*>(h + row * p.I + c0 + 4 * j) =
+              e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
+          if (j % 8 == 0) h_scale[row * (p.I / 32) + (c0 + 4 * j) / 32] = (uint8_t)(be + 127);
+        }
       }
-      mx = max(mx, dpp_u32<0xB1>(mx));   // lane ^ 1
-      mx = max(mx, dpp_u32<0x4E>(mx));   // lane ^ 2
-      mx = max(mx, dpp_u32<0x141>(mx));  // the other four of eight lanes
-      const int be = mx_block_exp_bits(mx);
-      const float inv = mx_inv_scale(be);
-      if (i < my.count) {
-        const int64_t row = my.row(shared, i);
-        *reinterpret_cast<uint32_t*>(h + row * p.I + c0 + 4 * j) =
-            e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
-        if (j % 8 == 0) h_scale[row * (p.I / 32) + (c0 + 4 * j) / 32] = (uint8_t)(be + 127);
-      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
                                                       const uint8_t* h, const uint8_t* h_scale,
                                                       float* __restrict__ o) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
-  constexpr int kCols = 16 * TILES;
+  constexpr int kCols = 16 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
   const int wave = wave_id(), r = threadIdx.x & 15;
   Served<DIRECT> my;
   if (!my.begin(p, offsets, p.d / kCols) || my.part * 16 * NT >= my.count) return;
@@ -402,16 +407,19 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
     }
     f32x4 acc[TILES][NT] = {};
     shared.product(ring, x, xo, xso, wave, (my.count - n0 + 15) / 16, acc);
-    shared.put(wave, acc);
-    __syncthreads();
-    // four columns of a token each
-    for (int q = threadIdx.x; q < 16 * NT * (kCols / 4); q += 256) {
-      const int j = q % (kCols / 4), token = q / (kCols / 4), i = n0 + token;
-      if (i < my.count)
-        *reinterpret_cast<f32x4*>(o + (int64_t)my.row(shared, i) * p.d + c0 + 4 * j) =
-            shared.get(token >> 4, j, token & 15);
+#pragma unroll
+    for (int n1 = 0; n1 < NT; n1 += kAtOnce) {
+      shared.put(wave, n1, acc);
+      __syncthreads();
+      // four columns of a token each
+      for (int q = threadIdx.x; q < 16 * kAtOnce * (kCols / 4); q += 256) {
+        const int j = q % (kCols / 4), token = q / (kCols / 4), i = n0 + 16 * n1 + token;
+        if (i < min(my.count, n0 + 16 * NT))
+          *reinterpret_cast<f32x4*>(o + (int64_t)my.row(shared, i) * p.d + c0 + 4 * j) =
+              shared.get(token >> 4, j, token & 15);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -498,30 +506,45 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
 }
 
 // y[t] = y_add[t] + sum_j w_j o[row_j] over the present routes in slot order;
-// token_row null: o has a row per route.
+// token_row null: o has a row per route.  The rows of eight routes are in
+// flight before the first is added.
 __global__ void __launch_bounds__(256) weighted_sum_kernel(RoutedFfn p, const int32_t* __restrict__ token_row,
                                                            const float* __restrict__ o) {
+  constexpr int kRoutes = 8;
   const int per = (p.d + 1023) / 1024;  // workgroup steps of a token
   for (int64_t b = blockIdx.x; b < p.T * per; b += gridDim.x) {
     const int64_t t = b / per;
     const int c = ((int)(b - t * per) * 256 + (int)threadIdx.x) * 4;
     if (c >= p.d) continue;
+    Slot<false, 4> add;
+    if (p.y_add) add = load_slot<false, false, false, 4>(p.y_add, t * p.d + c, 4);
     f32x4 acc = {};
-    for (int j = 0; j < p.k; ++j) {
-      int64_t row = t * p.k + j;
-      if (token_row)
-        row = token_row[row];
-      else if ((unsigned)p.topk_idx[row] >= (unsigned)p.E)
-        row = -1;
-      if (row < 0) continue;
-      const float g = p.topk_w[t * p.k + j];
-      const f32x4 v = *reinterpret_cast<const f32x4*>(o + row * p.d + c);
+    for (int j0 = 0; j0 < p.k; j0 += kRoutes) {
+      int64_t row[kRoutes];
+      f32x4 v[kRoutes];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(g, v[i], acc[i]);
+      for (int j = 0; j < kRoutes; ++j) {
+        row[j] = j0 + j < p.k ? t * p.k + j0 + j : -1;
+        if (row[j] < 0) continue;
+        if (token_row)
+          row[j] = token_row[row[j]];
+        else if ((unsigned)p.topk_idx[row[j]] >= (unsigned)p.E)
+          row[j] = -1;
+      }
+#pragma unroll
+      for (int j = 0; j < kRoutes; ++j)
+        if (row[j] >= 0) v[j] = *reinterpret_cast<const f32x4*>(o + row[j] * p.d + c);
+#pragma unroll
+      for (int j = 0; j < kRoutes; ++j) {
+        if (row[j] < 0) continue;
+        const float g = p.topk_w[t * p.k + j0 + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(g, v[j][i], acc[i]);
+      }
     }
     if (p.y_add) {
       float v[4];
-      unpack_slot(load_slot<false, false, false, 4>(p.y_add, t * p.d + c, 4), v);
+      unpack_slot(add, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += v[i];
     }
@@ -578,15 +601,18 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
 //   16                            393.7 391.8    8                          97.7  99.4
 constexpr int64_t kRepeats = 500000000;
 
-// Which tiles, after the schedule.  128 rows against 32 tokens read each token
-// half as often as 64 rows do (333 tokens, 128 experts of 4,096 x 1,536: 268 us,
-// 294; 300, 4 of 4,096 x 2,048, k = 2: 77, 83), 64 rows give twice the
-// workgroups where those are few (64 tokens, one expert of 7,168 x 2,048: 45,
-// 35; 16 tokens, 8 of 4,096 x 1,536: 31.5, 29.6).  An expert's tokens are
-// shared by as many workgroups as the mean calls for (512 tokens, one expert
-// of 7,168 x 2,048: 532 us with one, 87 with sixteen).
-constexpr int kTokenTiles = 2;
-constexpr int64_t kFewGroups = 512;
+// Which tiles, after the schedule.  An expert's tokens are shared by as many
+// workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 532
+// us with one, 88 with sixteen).
+//   128 weight rows against 48 tokens, from a mean of 24 tokens an expert on:
+//     most experts' tokens are then together and their weights read once (32
+//     experts of 7,168 x 2,048, 128 tokens of eight: 192 us, with 32 tokens at a
+//     time 254; 96 tokens 174 and 171).
+//   128 against 32: each token read half as often as by 64 rows (333 tokens, 128
+//     experts of 4,096 x 1,536: 268, 294).
+//   64 against 32 where workgroups are few, for twice as many (64 tokens, one
+//     expert of 7,168 x 2,048: 45, 35; 16 tokens, 8 of 4,096 x 1,536: 31.5, 29.6).
+constexpr int64_t kManyTokens = 24, kFewGroups = 512;
 
 hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const Scratch b = carve(static_cast<char*>(scratch), p.T, p.d, p.E, p.k, p.I);
@@ -607,20 +633,29 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const hipError_t e = launch_sort(false, p.topk_idx, nullptr, p.T, p.d, p.E, p.k, b.counts, b.offsets, b.row_token,
                                    b.token_row, nullptr, b.sort, s);
   if (e != hipSuccess) return e;
-  const int64_t want = ceil_div(R, (int64_t)p.E * 16 * kTokenTiles);
   const int64_t most = (1 << 22) / (p.I / 32 + p.d / 64);  // workgroups in x: threads stay below 2^32
-  const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(want, std::min<int64_t>(most, 64)));
-  auto tiles = [&](auto TILES) {
-    constexpr int t = TILES.value;
-    gate_up_kernel<t, kTokenTiles, false><<<dim3((unsigned)(p.I / (8 * t) * parts), (unsigned)p.E), 256, 0, s>>>(
+  auto parts = [&](int nt) {
+    return std::max<int64_t>(1, std::min<int64_t>({ceil_div(R, (int64_t)p.E * 16 * nt), most, 64}));
+  };
+  auto groups = [&](int nt) { return p.E * (p.I / 64) * parts(nt); };
+  auto run = [&](auto TILES, auto NT) {
+    constexpr int t = TILES.value, nt = NT.value;
+    const int64_t n = parts(nt);
+    gate_up_kernel<t, nt, false><<<dim3((unsigned)(p.I / (8 * t) * n), (unsigned)p.E), 256, 0, s>>>(
         p, b.offsets, b.row_token, b.h, b.h_scale);
-    down_kernel<t, kTokenTiles, false><<<dim3((unsigned)(p.d / (16 * t) * parts), (unsigned)p.E), 256, 0, s>>>(
+    down_kernel<t, nt, false><<<dim3((unsigned)(p.d / (16 * t) * n), (unsigned)p.E), 256, 0, s>>>(
         p, b.offsets, b.h, b.h_scale, b.o);
   };
-  if ((int64_t)p.E * (p.I / 64) * parts < kFewGroups)
-    tiles(std::integral_constant<int, 4>());
+  constexpr std::integral_constant<int, 2> two;
+  constexpr std::integral_constant<int, 3> three;
+  constexpr std::integral_constant<int, 4> four;
+  constexpr std::integral_constant<int, 8> eight;
+  if (R >= kManyTokens * p.E && groups(three) >= kFewGroups)
+    run(eight, three);
+  else if (groups(two) >= kFewGroups)
+    run(eight, two);
   else
-    tiles(std::integral_constant<int, 8>());
+    run(four, two);
   weighted_sum_kernel<<<sums, 256, 0, s>>>(p, b.token_row, b.o);
   return hipGetLastError();
 }

@@ -529,10 +529,9 @@ auto row_kernel(bool f32, int d, bool stream, Pick pick) {
 //     1                   6.8   7.5     7.5     7.6      7.7      7.9
 // The limits suit 64 experts and more with the rows copied (65,536 routes of
 // 256 experts with rows of 7,168: wide 200, three launches 197).  They are not
-// the best for a schedule alone of 2,048 routes (few, where wide is 3 us
-// faster), nor for 16,384 to 32,768 routes of very few experts, whose LDS
-// counters collide (wide, where three launches are up to 24 us faster).
-constexpr int64_t kFewRoutes = 2048, kWideLimit = 32768;
+// the best for 16,384 to 32,768 routes of very few experts, whose LDS counters
+// collide (wide, where three launches are up to 24 us faster).
+constexpr int64_t kFewRoutes = 2048, kFewAlone = 512, kWideLimit = 32768;
 
 size_t sort_scratch_bytes(int64_t T, int k, int E) {
   return (size_t)ceil_div(T * k, kSortRoutes) * (size_t)E * sizeof(int32_t);
@@ -548,7 +547,7 @@ hipError_t sort_rows(bool f32, const int32_t* topk_idx, const void* x, int64_t T
     return hipGetLastError();
   }
   const int64_t R = T * k;
-  if (R <= kFewRoutes) {
+  if (R <= (x_perm ? kFewRoutes : kFewAlone)) {
     const int slots = (int)ceil_div(d, f32 ? 4 : 8);
     const int th = slots <= 256 ? 256 : slots >= 1024 ? 1024 : (slots + 63) / 64 * 64;
     auto kernel = row_kernel(f32, d, false, [](auto F32, auto TAIL, auto) {
