@@ -506,37 +506,32 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
 }
 
 // y[t] = y_add[t] + sum_j w_j o[row_j] over the present routes in slot order;
-// token_row null: o has a row per route.  The rows of eight routes are in
-// flight before the first is added.
+// DIRECT: o has a row per route.  The rows of eight routes are in flight before
+// the first is added.
+template <bool DIRECT>
 __global__ void __launch_bounds__(256) weighted_sum_kernel(RoutedFfn p, const int32_t* __restrict__ token_row,
                                                            const float* __restrict__ o) {
   constexpr int kRoutes = 8;
   const int per = (p.d + 1023) / 1024;  // workgroup steps of a token
+  const int32_t* ids = DIRECT ? p.topk_idx : token_row;
   for (int64_t b = blockIdx.x; b < p.T * per; b += gridDim.x) {
-    const int64_t t = b / per;
-    const int c = ((int)(b - t * per) * 256 + (int)threadIdx.x) * 4;
+    const int t = (int)(b / per), c = ((int)(b - (int64_t)t * per) * 256 + (int)threadIdx.x) * 4;
     if (c >= p.d) continue;
     Slot<false, 4> add;
-    if (p.y_add) add = load_slot<false, false, false, 4>(p.y_add, t * p.d + c, 4);
+    if (p.y_add) add = load_slot<false, false, false, 4>(p.y_add, (int64_t)t * p.d + c, 4);
     f32x4 acc = {};
     for (int j0 = 0; j0 < p.k; j0 += kRoutes) {
-      int64_t row[kRoutes];
+      bool here[kRoutes];
       f32x4 v[kRoutes];
 #pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
-        row[j] = j0 + j < p.k ? t * p.k + j0 + j : -1;
-        if (row[j] < 0) continue;
-        if (token_row)
-          row[j] = token_row[row[j]];
-        else if ((unsigned)p.topk_idx[row[j]] >= (unsigned)p.E)
-          row[j] = -1;
+        const int r = t * p.k + j0 + j, id = j0 + j < p.k ? ids[r] : -1;
+        here[j] = DIRECT ? (unsigned)id < (unsigned)p.E : id >= 0;
+        if (here[j]) v[j] = *reinterpret_cast<const f32x4*>(o + (int64_t)(DIRECT ? r : id) * p.d + c);
       }
 #pragma unroll
-      for (int j = 0; j < kRoutes; ++j)
-        if (row[j] >= 0) v[j] = *reinterpret_cast<const f32x4*>(o + row[j] * p.d + c);
-#pragma unroll
       for (int j = 0; j < kRoutes; ++j) {
-        if (row[j] < 0) continue;
+        if (!here[j]) continue;
         const float g = p.topk_w[t * p.k + j0 + j];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = fmaf(g, v[j][i], acc[i]);
@@ -549,7 +544,7 @@ __global__ void __launch_bounds__(256) weighted_sum_kernel(RoutedFfn p, const in
       for (int i = 0; i < 4; ++i) acc[i] += v[i];
     }
     const float out[4] = {acc[0], acc[1], acc[2], acc[3]};
-    store_slot<false, false, false, 4>(p.y, t * p.d + c, 4, pack_slot<false>(out));
+    store_slot<false, false, false, 4>(p.y, (int64_t)t * p.d + c, 4, pack_slot<false>(out));
   }
 }
 
@@ -627,7 +622,7 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
       return hipGetLastError();
     }
     down_kernel<4, 1, true><<<dim3(p.d / 64, routes), 256, 0, s>>>(p, nullptr, b.h, b.h_scale, b.o);
-    weighted_sum_kernel<<<sums, 256, 0, s>>>(p, nullptr, b.o);
+    weighted_sum_kernel<true><<<sums, 256, 0, s>>>(p, nullptr, b.o);
     return hipGetLastError();
   }
   const hipError_t e = launch_sort(false, p.topk_idx, nullptr, p.T, p.d, p.E, p.k, b.counts, b.offsets, b.row_token,
@@ -656,7 +651,7 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
     run(eight, two);
   else
     run(four, two);
-  weighted_sum_kernel<<<sums, 256, 0, s>>>(p, b.token_row, b.o);
+  weighted_sum_kernel<false><<<sums, 256, 0, s>>>(p, b.token_row, b.o);
   return hipGetLastError();
 }
 
