@@ -19,7 +19,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 4;      // of a workgroup, which share the K of a tile
+constexpr int kWaves = 4;  // of a workgroup, which share the K of a tile
 // Routes up to which a workgroup finds its expert's tokens by itself, with a
 // workgroup for every route: where there are as many experts as routes, or one
 // tile holds all tokens.  It saves the schedule (8 tokens, one expert of 7,168 x
@@ -56,7 +56,7 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Loads before are issued before, loads behind behind: waits count them.
+// What is written before is issued before: waits count loads in their order.
 __device__ __forceinline__ void in_order() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
@@ -238,21 +238,27 @@ struct Shared {
     wait_loads<0>();  // the ring is free again
     in_order();
   }
-  // [rows' tile, tokens' tile][4 rows, token] of the tokens' tiles from n0 on.
+  // Where a wave's sum of rows 4 j to 4 j + 3 for token r of tokens' tile n
+  // lies.  The token's place is turned by j, so that neither neighbouring j of
+  // a token nor neighbouring tokens of a j meet in one bank when they are read.
+  __device__ __forceinline__ int place(int n, int j, int r) const {
+    return ((j / 4) * kAtOnce + n) * 64 + (j % 4) * 16 + (r ^ (j & 15) ^ ((j & 1) << 3));
+  }
+  // The sums of the tokens' tiles from n0 on.
   __device__ __forceinline__ void put(int w, int n0, const f32x4 (&acc)[TILES][NT]) {
-    f32x4* to = reinterpret_cast<f32x4*>(wave(w)) + (threadIdx.x & 63);
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int m = 0; m < TILES; ++m)
 #pragma unroll
       for (int n = 0; n < kAtOnce; ++n)
-        if (n0 + n < NT) to[(m * kAtOnce + n) * 64] = acc[m][n0 + n];
+        if (n0 + n < NT)
+          reinterpret_cast<f32x4*>(wave(w))[place(n, 4 * m + (lane >> 4), lane & 15)] = acc[m][n0 + n];
   }
   // Rows 4 j to 4 j + 3 of the tile for token r of tokens' tile n0 + n, the waves' sums in order.
   __device__ __forceinline__ f32x4 get(int n, int j, int r) {
     f32x4 v = {};
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
-      v += reinterpret_cast<const f32x4*>(wave(w))[((j / 4) * kAtOnce + n) * 64 + (j % 4) * 16 + r];
+    for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const f32x4*>(wave(w))[place(n, j, r)];
     return v;
   }
 };
@@ -461,10 +467,8 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
     auto issue = [&](int i, int u) {
       uint8_t* to = lds + kRing + u * kToken;
       ring.issue(i, u);
-      if (lane < 16)
-        lds_dma<16>(x.rsrc(), to, lane * 16, i * 256);
-      if (lane < 2)
-        lds_dma<4>(xs.rsrc(), to + 256, lane * 4, i * 8);
+      if (lane < 16) lds_dma<16>(x.rsrc(), to, lane * 16, i * 256);
+      if (lane < 2) lds_dma<4>(xs.rsrc(), to + 256, lane * 4, i * 8);
     };
     f32x4 acc[kWaves] = {};
     auto multiply = [&](int u, int stage, int slab) {
@@ -473,7 +477,10 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
                    *reinterpret_cast<const u32x4*>(x + 64), lds[kRing + stage * kToken + 256 + slab * 4 + g], acc[u]);
     };
 #pragma unroll
-    for (int u = 0; u < kTokenStages; ++u) issue(u, u);
+    for (int u = 0; u < kTokenStages; ++u) {
+      in_order();
+      issue(u, u);
+    }
     for (int q = 0; q < ring.pairs; q += kWaves) {
 #pragma unroll
       for (int u = 0; u < kWaves; ++u) {
