@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
       // eight lanes per token and 32 columns, four columns each
       for (int q = threadIdx.x >> 3; q < 16 * kAtOnce * (kCols / 32); q += 32) {
         const int token = q % (16 * kAtOnce), j = q / (16 * kAtOnce) * 8 + (lane & 7), i = n0 + 16 * n1 + token;
+        if (i >= min(my.count, n0 + 16 * NT)) continue;
         const f32x4 gate = shared.get(token >> 4, j, token & 15);
         const f32x4 up = shared.get(token >> 4, kCols / 4 + j, token & 15);
         float z[4];
@@ -370,12 +371,10 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
         mx = max(mx, dpp_u32<0x141>(mx));  // the other four of eight lanes
         const int be = mx_block_exp_bits(mx);
         const float inv = mx_inv_scale(be);
-        if (i < min(my.count, n0 + 16 * NT)) {
-          const int64_t row = my.row(shared, i);
-          *reinterpret_cast<uint32_t*>(h + row * p.I + c0 + 4 * j) =
-              e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
-          if (j % 8 == 0) h_scale[row * (p.I / 32) + (c0 + 4 * j) / 32] = (uint8_t)(be + 127);
-        }
+        const int64_t row = my.row(shared, i);
+        *reinterpret_cast<uint32_t*>(h + row * p.I + c0 + 4 * j) =
+            e4m3x4_rne_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv);
+        if (j % 8 == 0) h_scale[row * (p.I / 32) + (c0 + 4 * j) / 32] = (uint8_t)(be + 127);
       }
       __syncthreads();
     }
