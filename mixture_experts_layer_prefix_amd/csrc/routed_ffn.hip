@@ -66,7 +66,9 @@ __device__ __forceinline__ void in_order() {
 // slabs (256 of K).  Codes: direct loads to LDS of eight rows' whole 128-byte
 // lines, which the streaming hint needs (1.6 GB read so reach 7.0 TB/s, without
 // the hint 6.3; as sixteen rows of half a line with the hint 5.0), and which
-// hold no registers while they are under way.  A lane's 16 bytes are put in a
+// hold no registers while they are under way.  Without the hint are weights
+// that several workgroups or rounds read, which are to stay in L2 (512 tokens
+// of eight, 32 experts of 7,168 x 2,048: 447 us, all with the hint 503).  A lane's 16 bytes are put in a
 // place turned by its row, so that the reads of sixteen rows of a slab meet no
 // bank twice.  Scales: a word per row and slab.
 template <int TILES, int STAGES>
@@ -83,10 +85,12 @@ struct Ring {
   uint32_t ld, ws_step;            // bytes of eight rows' codes, between slabs of scales
   uint32_t read, read_scale;       // a lane's place in a stage
   int pairs;
+  bool again;                      // the weights are read more than once
 
-  __device__ __forceinline__ void begin(uint8_t* ring, int K, int64_t all_rows) {
+  __device__ __forceinline__ void begin(uint8_t* ring, int K, int64_t all_rows, bool reread) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     lds = ring;
+    again = reread;
     pairs = (K + 255) / 256;
     ld = 4 * K;
     ws_step = (uint32_t)all_rows * 4;
@@ -101,14 +105,21 @@ struct Ring {
     w[i] = {codes + row * (K / 2), (uint32_t)kRows * (K / 2)};
     ws[i] = {scales + row * 4, ws_step * (K / 128) - (uint32_t)row * 4};
   }
-  // Starts the loads of pair i into its stage; past the last pair they read nothing.
-  __device__ __forceinline__ void issue(int i, int stage) const {
-    uint8_t* to = lds + stage * kStage;
+  template <int AUX>
+  __device__ __forceinline__ void issue_codes(int i, uint8_t* to) const {
 #pragma unroll
     for (int j = 0; j < 2 * TILES; ++j) {
       const int m = j / (2 * TILES / kMats), q = j % (2 * TILES / kMats);
-      lds_dma<16, 2>(w[m].rsrc(), to + j * 1024, j & 1 ? odd : even, i < pairs ? i * 128 + q * ld : w[m].n);
+      lds_dma<16, AUX>(w[m].rsrc(), to + j * 1024, j & 1 ? odd : even, i < pairs ? i * 128 + q * ld : w[m].n);
     }
+  }
+  // Starts the loads of pair i into its stage; past the last pair they read nothing.
+  __device__ __forceinline__ void issue(int i, int stage) const {
+    uint8_t* to = lds + stage * kStage;
+    if (again)
+      issue_codes<0>(i, to);
+    else
+      issue_codes<2>(i, to);
     if (2 * kRows < 64 && (threadIdx.x & 63) >= 2 * kRows) return;
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
   if (!my.begin(p, offsets, p.I / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
-  ring.begin(shared.wave(wave), p.d, (int64_t)p.E * p.I);
+  ring.begin(shared.wave(wave), p.d, (int64_t)p.E * p.I, !DIRECT && my.count > 16 * NT);
   ring.rows(0, p.w.q_gate, p.w.q_gate_scale, (int64_t)my.e * p.I + c0, p.d);
   ring.rows(1, p.w.q_up, p.w.q_up_scale, (int64_t)my.e * p.I + c0, p.d);
   ring.issue(wave, 0);  // the first weights are under way while the tokens are found
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
   if (!my.begin(p, offsets, p.d / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
-  ring.begin(shared.wave(wave), p.I, (int64_t)p.E * p.d);
+  ring.begin(shared.wave(wave), p.I, (int64_t)p.E * p.d, !DIRECT && my.count > 16 * NT);
   ring.rows(0, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0, p.I);
   ring.rows(1, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0 + kCols / 2, p.I);
   ring.issue(wave, 0);
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
   const bool odd = (p.I / 128) & 1;
   uint8_t* lds = shared.rings[wave];
   R ring;
-  ring.begin(lds, p.I, (int64_t)p.E * p.d);
+  ring.begin(lds, p.I, (int64_t)p.E * p.d, false);
   for (int j = wave; j < p.k; j += waves) {
     const int e = __builtin_amdgcn_readfirstlane(p.topk_idx[t * p.k + j]);
     if ((unsigned)e >= (unsigned)p.E) continue;
