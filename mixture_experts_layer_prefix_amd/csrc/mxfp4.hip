@@ -5,10 +5,13 @@
 // clamped to [-127, 127]; an element is v / 2^e rounded to nearest even, sign
 // kept.  v / 2^e is exact, so there is one rounding.
 //
-// Both directions touch every byte once and are bound by memory.  Sixteen
+// Both directions touch every byte once and are bound by memory: 65,536 x
+// 7,168 to 4 bits in 215 us (5.5 TB/s), back in 173 (6.9 TB/s).  Sixteen
 // lanes take the 128 columns of a slab, eight each, so that a row's four
 // scales form a word in one exchange inside the lanes' row, and sixteen rows
-// write 64 consecutive bytes of the slab-major scales.
+// write 64 consecutive bytes of the slab-major scales.  Sixteen columns a
+// thread, so that a wave's codes fill whole cache lines, took 235 and 485 us:
+// the reads and writes of bf16 then fill half a line each.
 #include "mxfp4.h"
 #include "rows.h"
 

@@ -8,7 +8,12 @@
 // the weights' bytes bound the time.  The weights stay in 4 bits up to the
 // matrix cores: v_mfma_scale_f32_16x16x128_f8f6f4 takes E2M1 weights and E4M3
 // activations with their block scales as they lie in memory, sixteen weight
-// rows against sixteen tokens.
+// rows against sixteen tokens.  One token through 8 of 256 experts of 7,168 x
+// 2,048 takes 37 us for 187 MB (5.1 TB/s, two launches; the gate and up
+// projections by themselves 5.4 TB/s), sixteen tokens 391 for 2.4 GB (6.1
+// TB/s).  From a mean of some 40 tokens an expert on the matrix cores' feeding
+// from LDS bounds it instead (512 tokens of eight, 32 experts: 447 us, 0.8
+// PFLOP/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -23,9 +28,9 @@ constexpr int kWaves = 4;  // of a workgroup, which share the K of a tile
 // Routes up to which a workgroup finds its expert's tokens by itself, with a
 // workgroup for every route: where there are as many experts as routes, or one
 // tile holds all tokens.  It saves the schedule (8 tokens, one expert of 7,168 x
-// 2,048: 25 us, after a schedule 35; 4 tokens, 8 of 2,048 x 768, k = 4: 17, 25),
-// but reads sixteen tokens at a time (16 tokens, 8 of 4,096 x 1,536, k = 2: 36,
-// after a schedule 33).
+// 2,048: 24.4 us, after a schedule 26.0; 4 tokens, 8 of 2,048 x 768, k = 4: 16.1,
+// 20.5), but reads sixteen tokens at a time and starts a workgroup for every
+// route (16 tokens, 8 of 4,096 x 1,536, k = 2: 35.2, after a schedule 28.7).
 constexpr int kDirect = 1024;
 
 // The wave's number in its workgroup, in a scalar register.
@@ -68,9 +73,9 @@ __device__ __forceinline__ void in_order() {
 // the hint 6.3; as sixteen rows of half a line with the hint 5.0), and which
 // hold no registers while they are under way.  Without the hint are weights
 // that several workgroups or rounds read, which are to stay in L2 (512 tokens
-// of eight, 32 experts of 7,168 x 2,048: 447 us, all with the hint 503).  A lane's 16 bytes are put in a
-// place turned by its row, so that the reads of sixteen rows of a slab meet no
-// bank twice.  Scales: a word per row and slab.
+// of eight, 32 experts of 7,168 x 2,048: 447 us, all with the hint 503).  A
+// lane's 16 bytes are put in a place turned by its row, so that the reads of
+// sixteen rows of a slab meet no bank twice.  Scales: a word per row and slab.
 template <int TILES, int STAGES>
 struct Ring {
   static constexpr int kCodes = TILES * 2048, kScales = TILES * 128, kStage = kCodes + kScales;
@@ -212,8 +217,8 @@ struct Shared {
   // and the first `tiles` (up to NT) times sixteen tokens; the first pair's
   // weights are under way.  No barrier: the ring is the wave's own.  One pair
   // of each wave is in flight: 8.5 or 17 KB, 139 KB on a compute unit with the
-  // sixteen or eight waves that fit.  Two stages of half as many waves: 8.5 KB
-  // stages 422 us where one takes 414 (16 tokens, 256 experts of 7,168 x 2,048).
+  // sixteen or eight waves that fit.  Two stages of half as many waves took 2%
+  // longer (16 tokens, 256 experts of 7,168 x 2,048).
   __device__ __forceinline__ void product(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
                                           const uint32_t (&xso)[NT], int first, int tiles,
                                           f32x4 (&acc)[TILES][NT]) const {
@@ -441,8 +446,8 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
 
 constexpr int kDownWaves = 8;
 // Two stages let four workgroups onto a compute unit (four stages two of them,
-// with as much in flight: 4 tokens, 256 experts of 7,168 x 2,048, 123 us, with
-// two 116; 5 tokens, 64 of 2,048 x 768, 24.5, 21.7).
+// with as much in flight: 4 tokens, 256 experts of 7,168 x 2,048, 121.8 us, with
+// two 114.2; 5 tokens, 64 of 2,048 x 768, 24.0, 21.0).
 constexpr int kTokenStages = 2;
 
 // A token's sixteen columns of y, h with a row per route: each wave takes the
@@ -606,24 +611,25 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
 // that chose it: R^2 / 2E experts for R routes at random, weighed here in
 // weights.  us of the whole call, by token and by expert (tokens, experts of d x
 // I, k):
-//   1, 256 of 7,168 x 2,048, 8    39.0  -        2, 64 of 2,048 x 768, 6    17.5  23.2
-//   2                             63.7  70.7     5                          21.5  26.2
-//   4                             116.0 120.9    10                         35.5  38.0
-//   8                             213.5 216.2    4, 128 of 4,096 x 1,536, 8 56.5  62.0
-//   16                            393.7 391.8    8                          97.7  99.4
+//   1, 256 of 7,168 x 2,048, 8    38.3  -        2, 64 of 2,048 x 768, 6    16.2  21.3
+//   2                             63.0  69.0     5                          20.9  25.0
+//   4                             114.0 119.3    10                         34.8  37.1
+//   8                             211.9 214.1    4, 128 of 4,096 x 1,536, 8 55.7  60.8
+//   16                            392.4 390.5    8                          97.0  97.9
 constexpr int64_t kRepeats = 500000000;
 
 // Which tiles, after the schedule.  An expert's tokens are shared by as many
-// workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 532
-// us with one, 88 with sixteen).
+// workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 306
+// us with one, 73 with sixteen).
 //   128 weight rows against 48 tokens, from a mean of 24 tokens an expert on:
 //     most experts' tokens are then together and their weights read once (32
-//     experts of 7,168 x 2,048, 128 tokens of eight: 192 us, with 32 tokens at a
-//     time 254; 96 tokens 174 and 171).
+//     experts of 7,168 x 2,048, 128 tokens of eight: 182 us, with 32 tokens at a
+//     time 230; 96 tokens 165 and 161).
 //   128 against 32: each token read half as often as by 64 rows (333 tokens, 128
-//     experts of 4,096 x 1,536: 268, 294).
+//     experts of 4,096 x 1,536: 273 us, 307).
 //   64 against 32 where workgroups are few, for twice as many (64 tokens, one
-//     expert of 7,168 x 2,048: 45, 35; 16 tokens, 8 of 4,096 x 1,536: 31.5, 29.6).
+//     expert of 7,168 x 2,048: 31.6 us, by 128 rows 39.2; 16 tokens, 8 of 4,096 x
+//     1,536: 29.0, 30.5).
 constexpr int64_t kManyTokens = 24, kFewGroups = 512;
 
 hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
