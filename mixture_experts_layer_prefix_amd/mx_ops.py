@@ -39,9 +39,6 @@ class BlockNormMxfp8Plan(BlockNormPlan):
             self.r_pre = torch.empty(block.T, dtype=_F32, device=self.device)
         self.a_q = torch.empty(block.T, block.d, dtype=_U8, device=self.device)
         self.a_scale = torch.empty(block.T, block.d // 32, dtype=_U8, device=self.device)
-        self._x_out = None if self.x_out is None else self.x_out.data_ptr()
-        self._outputs = [None if t is None else t.data_ptr()
-                         for t in (self.a, self.a_q, self.a_scale, self.r_post, self.r_pre)]
 
     def run(self, x, y=None, w_pre=None, w_post=None, gate=None):
         """(x_out, a_q, a_scale); x_out is x itself where there is no block
@@ -49,7 +46,9 @@ class BlockNormMxfp8Plan(BlockNormPlan):
         dev = self.device
         px, py = _given("x", x, self._res, self._rows, dev), _check("y", y, self._act, self._rows, dev)
         _launch(dev, "moe_block_norm_mxfp8", self.cblock, px, py, *self._vectors(w_pre, w_post, gate),
-                None if y is None else self._x_out, *self._outputs)
+                None if y is None or self.x_out is None else self.x_out.data_ptr(),
+                None if self.a is None else self.a.data_ptr(), self.a_q.data_ptr(), self.a_scale.data_ptr(),
+                None if self.r_post is None else self.r_post.data_ptr(), self.r_pre.data_ptr())
         return (x if y is None else self.x_out), self.a_q, self.a_scale
 
 
@@ -87,8 +86,6 @@ class SortMxfp8Plan:
         self._ids, self._rows, self._scales = (dims.T, dims.k), (dims.T, dims.d), (dims.T, dims.d // 32)
         self.ws_bytes = n.value
         self.ws = torch.empty(max(n.value, 16), dtype=_U8, device=dev)
-        self._outputs = [t.data_ptr() for t in (self.counts, self.offsets, self.row_token, self.token_row,
-                                                self.x_perm, self.x_perm_scale, self.ws)]
 
     def run(self, topk_idx, x, x_scale):
         """(counts, offsets, row_token, token_row, x_perm, x_perm_scale) of the
@@ -96,7 +93,9 @@ class SortMxfp8Plan:
         dev = self.device
         args = (_given("topk_idx", topk_idx, _I32, self._ids, dev), _given("x", x, _U8, self._rows, dev),
                 _given("x_scale", x_scale, _U8, self._scales, dev))
-        _launch(dev, "moe_sort_tokens_mxfp8", self.cdims, *args, *self._outputs, self.ws_bytes)
+        _launch(dev, "moe_sort_tokens_mxfp8", self.cdims, *args, self.counts.data_ptr(), self.offsets.data_ptr(),
+                self.row_token.data_ptr(), self.token_row.data_ptr(), self.x_perm.data_ptr(),
+                self.x_perm_scale.data_ptr(), self.ws.data_ptr(), self.ws_bytes)
         return self.counts, self.offsets, self.row_token, self.token_row, self.x_perm, self.x_perm_scale
 
 

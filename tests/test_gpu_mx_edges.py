@@ -83,6 +83,54 @@ def test_routed_ffn_experts_beyond_4_gb():
         assert torch.equal(got, want[:t])
 
 
+@pytest.mark.parametrize("T,d,E,k,I", [(600, 256, 8, 1, 128), (700, 128, 900, 1, 256), (1500, 128, 40, 1, 128)])
+def test_routed_ffn_every_token_at_one_expert(T, d, E, k, I):
+    """More tokens at one expert than its share of the workgroups takes at a
+    time, with a schedule and without."""
+    x, xs, w = whole_problem(T, T, d, E, k, I)
+    idx = torch.full((T, k), E // 2, dtype=I32, device="cuda")
+    tw = torch.rand(T, k, generator=gen(3), device="cuda")
+    y = poisoned(M.Dims(T, d, E, k, I)).run(x, xs, idx, tw, w)
+    few, mine, names = used_experts(w, idx, E, None)
+    want, bound = reference(x, xs, mine, tw, few, len(names), exact_gu=True)
+    off = np.abs(np64(y) - want)
+    assert np.all(off <= bound), (off / bound).max()
+
+
+def test_routed_ffn_one_expert_by_expert():
+    T, d, E, k, I = 512, 1024, 512, 1, 1024
+    x, xs, w = real_problem(13, T, d, E, k, I)
+    idx = torch.full((T, k), 77, dtype=I32, device="cuda")
+    idx[100:110] = 3
+    tw = torch.rand(T, k, generator=gen(2), device="cuda")
+    y = poisoned(M.Dims(T, d, E, k, I)).run(x, xs, idx, tw, w)
+    one = M.RoutedFfnPlan(M.Dims(1, d, E, k, I))
+    for t in (0, 15, 16, 99, 105, 300, 511):
+        s = slice(t, t + 1)
+        assert torch.equal(one.run(x[s], xs[s], idx[s], tw[s], w), y[s]), t
+
+
+def test_plans_write_the_tensors_that_they_hold():
+    """A plan's output may be replaced by another tensor of its shape between
+    two calls."""
+    T, d, E, k, I = 6, 256, 4, 2, 128
+    x, xs, w = real_problem(3, T, d, E, k, I)
+    idx, tw = ids(1, T, k, -1, E), torch.rand(T, k, generator=gen(2), device="cuda")
+    res, out = randn(1, (T, d)), randn(2, (T, d))
+    plans = [M.BlockNormMxfp8Plan(M.Block(T, d)), M.SortMxfp8Plan(M.Dims(T, d, E, k, 1)),
+             M.RoutedFfnPlan(M.Dims(T, d, E, k, I))]
+    calls = [lambda p: p.run(res, out), lambda p: p.run(idx, x, xs), lambda p: (p.run(x, xs, idx, tw, w),)]
+    for plan, run in zip(plans, calls):
+        if hasattr(plan, "x_perm"):
+            for t in (plan.row_token, plan.x_perm, plan.x_perm_scale):
+                t.zero_()
+        first = [t.clone() for t in run(plan)]
+        for name, t in list(vars(plan).items()):
+            if torch.is_tensor(t) and name != "ws":
+                setattr(plan, name, torch.zeros_like(t))
+        assert all(torch.equal(a, b) for a, b in zip(run(plan), first)), type(plan).__name__
+
+
 def test_two_plans_at_once():
     T, d, E, k, I = 40, 512, 8, 3, 256
     x, xs, w = real_problem(9, T, d, E, k, I)
