@@ -143,21 +143,45 @@ struct Ring {
   }
 };
 
-// Sixteen tokens' part of a pair of slabs, as loaded.
+// The dword of lane `from` / 4.
+__device__ __forceinline__ uint32_t of_lane(int from, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(from, (int)v);
+}
+__device__ __forceinline__ u32x4 of_lane(int from, u32x4 v) {
+  return u32x4{of_lane(from, v[0]), of_lane(from, v[1]), of_lane(from, v[2]), of_lane(from, v[3])};
+}
+
+// Sixteen tokens' part of a pair of slabs.  It is loaded with a token's 64
+// bytes in four lanes side by side, which cost the L1 cache one access, and
+// then dealt to the lanes that feed it.
 struct TokenPair {
   u32x4 lo[2], hi[2];
-  u32x2 xs;  // a word for each slab
+  uint32_t xs;  // scales of slab 0 in even lanes, of slab 1 in odd ones
+  __device__ __forceinline__ void deal() {
+    const int lane = threadIdx.x & 63, from = (lane & 15) * 16 + (lane >> 4) * 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      lo[u] = of_lane(from, lo[u]);
+      hi[u] = of_lane(from, hi[u]);
+    }
+  }
+  // The lane's scale of slab u.
+  __device__ __forceinline__ uint32_t scale(int u) const {
+    const int lane = threadIdx.x & 63;
+    return of_lane((lane & 15) * 16 + u * 4, xs) >> ((lane >> 4) * 8);
+  }
 };
 
 // Tokens [][K] in E4M3 and their scales.
 struct Tokens {
   Bytes x, xs;
   int K;
+  // Of a lane's loads of token lane / 4.
   __device__ __forceinline__ uint32_t offset(bool on, uint32_t row) const {
-    return on ? row * K + ((threadIdx.x & 63) >> 4) * 16 : x.n;
+    return on ? row * K + (threadIdx.x & 3) * 16 : x.n;
   }
   __device__ __forceinline__ uint32_t scale_offset(bool on, uint32_t row) const {
-    return on ? row * (K / 32) : xs.n;
+    return on ? row * (K / 32) + (threadIdx.x & 1) * 4 : xs.n;
   }
   // Pair i; the second slab of an odd last pair is not used.
   __device__ __forceinline__ void load(int i, uint32_t o, uint32_t so, TokenPair& t) const {
@@ -166,7 +190,7 @@ struct Tokens {
       t.lo[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o, i * 256 + u * 128, 0);
       t.hi[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o + 64, i * 256 + u * 128, 0);
     }
-    t.xs = __builtin_amdgcn_raw_buffer_load_b64(xs.rsrc(), so, i * 8, 0);
+    t.xs = __builtin_amdgcn_raw_buffer_load_b32(xs.rsrc(), so, i * 8, 0);
   }
 };
 
@@ -223,7 +247,6 @@ struct Shared {
                                           const uint32_t (&xso)[NT], int first, int tiles,
                                           f32x4 (&acc)[TILES][NT]) const {
     const bool odd = (x.K / 128) & 1;
-    const int shift = (threadIdx.x & 63) >> 4 << 3;  // of the lane's scale in a word
     TokenPair t[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -232,6 +255,14 @@ struct Shared {
       in_order();
       wait_loads<0>();
       in_order();
+      uint32_t xs[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= tiles) continue;
+        t[n].deal();
+        xs[n][0] = t[n].scale(0);
+        xs[n][1] = t[n].scale(1);
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (u == 1 && odd && i + 1 == ring.pairs) break;
@@ -241,7 +272,7 @@ struct Shared {
           const uint32_t ws = ring.scales(0, m, u);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (n < tiles) acc[m][n] = mma(w, ws, t[n].lo[u], t[n].hi[u], t[n].xs[u] >> shift, acc[m][n]);
+            if (n < tiles) acc[m][n] = mma(w, ws, t[n].lo[u], t[n].hi[u], xs[n][u], acc[m][n]);
         }
       }
       in_order();
@@ -340,7 +371,7 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
                                                          uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 8 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
-  const int lane = threadIdx.x & 63, wave = wave_id(), r = lane & 15;
+  const int lane = threadIdx.x & 63, wave = wave_id();
   Served<DIRECT> my;
   if (!my.begin(p, offsets, p.I / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
@@ -356,7 +387,7 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int i = n0 + 16 * n + r;
+      const int i = n0 + 16 * n + (threadIdx.x & 63) / 4;
       const bool on = i < my.count;
       const int row = on ? my.row(shared, i) : 0;
       const uint32_t t = !on ? 0 : DIRECT ? row / p.k : row_token[row];
@@ -404,7 +435,7 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
                                                       float* __restrict__ o) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 16 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
-  const int wave = wave_id(), r = threadIdx.x & 15;
+  const int wave = wave_id();
   Served<DIRECT> my;
   if (!my.begin(p, offsets, p.d / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
@@ -420,7 +451,7 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int i = n0 + 16 * n + r;
+      const int i = n0 + 16 * n + (threadIdx.x & 63) / 4;
       const bool on = i < my.count;
       const uint32_t row = on ? my.row(shared, i) : 0;
       xo[n] = x.offset(on, row);
