@@ -61,6 +61,9 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Reads of LDS that came before have arrived.
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
 // What is written before is issued before: waits count loads in their order.
 __device__ __forceinline__ void in_order() {
   asm volatile("" ::: "memory");
@@ -111,20 +114,26 @@ struct Ring {
     ws[i] = {scales + row * 4, ws_step * (K / 128) - (uint32_t)row * 4};
   }
   template <int AUX>
-  __device__ __forceinline__ void issue_codes(int i, uint8_t* to) const {
-#pragma unroll
-    for (int j = 0; j < 2 * TILES; ++j) {
-      const int m = j / (2 * TILES / kMats), q = j % (2 * TILES / kMats);
-      lds_dma<16, AUX>(w[m].rsrc(), to + j * 1024, j & 1 ? odd : even, i < pairs ? i * 128 + q * ld : w[m].n);
-    }
+  __device__ __forceinline__ void issue_tile(int i, int t, uint8_t* to) const {
+    const int m = t / (TILES / kMats), q = t % (TILES / kMats) * 2;
+    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048, even, i < pairs ? i * 128 + q * ld : w[m].n);
+    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048 + 1024, odd, i < pairs ? i * 128 + (q + 1) * ld : w[m].n);
   }
-  // Starts the loads of pair i into its stage; past the last pair they read nothing.
+  // Starts the loads of pair i into its stage, whole or in parts: the codes of
+  // tile t, the scales.  Past the last pair they read nothing.
   __device__ __forceinline__ void issue(int i, int stage) const {
-    uint8_t* to = lds + stage * kStage;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) issue_codes(i, stage, t);
+    issue_scales(i, stage);
+  }
+  __device__ __forceinline__ void issue_codes(int i, int stage, int t) const {
     if (again)
-      issue_codes<0>(i, to);
+      issue_tile<0>(i, t, lds + stage * kStage);
     else
-      issue_codes<2>(i, to);
+      issue_tile<2>(i, t, lds + stage * kStage);
+  }
+  __device__ __forceinline__ void issue_scales(int i, int stage) const {
+    uint8_t* to = lds + stage * kStage;
     if (2 * kRows < 64 && (threadIdx.x & 63) >= 2 * kRows) return;
 #pragma unroll
     for (int m = 0; m < kMats; ++m)
@@ -263,23 +272,38 @@ struct Shared {
         xs[n][0] = t[n].scale(0);
         xs[n][1] = t[n].scale(1);
       }
+      const bool two = !(odd && i + 1 == ring.pairs);  // slabs
+      u32x4 w[2][2];
+      uint32_t ws[2][2];
+      auto read = [&](int m) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        if (u == 1 && odd && i + 1 == ring.pairs) break;
+        for (int u = 0; u < 2; ++u) {
+          w[m & 1][u] = ring.codes(0, m, u);
+          ws[m & 1][u] = ring.scales(0, m, u);
+        }
+      };
+      read(0);
 #pragma unroll
-        for (int m = 0; m < TILES; ++m) {
-          const u32x4 w = ring.codes(0, m, u);
-          const uint32_t ws = ring.scales(0, m, u);
+      for (int m = 0; m < TILES; ++m) {
+        in_order();
+        wait_lds();
+        in_order();
+        ring.issue_codes(i + kWaves, 0, m);
+        in_order();
+        if (m + 1 < TILES) read(m + 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (u == 1 && !two) break;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            if (n < tiles) acc[m][n] = mma(w, ws, t[n].lo[u], t[n].hi[u], xs[n][u], acc[m][n]);
+            if (n < tiles) acc[m][n] = mma(w[m & 1][u], ws[m & 1][u], t[n].lo[u], t[n].hi[u], xs[n][u], acc[m][n]);
         }
       }
       in_order();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
         if (n < tiles) x.load(i + kWaves, xo[n], xso[n], t[n]);
-      ring.issue(i + kWaves, 0);
+      ring.issue_scales(i + kWaves, 0);
     }
     in_order();
     wait_loads<0>();  // the ring is free again
