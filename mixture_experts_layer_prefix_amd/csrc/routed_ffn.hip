@@ -252,22 +252,21 @@ struct Shared {
   // of each wave is in flight: 8.5 or 17 KB, 139 KB on a compute unit with the
   // sixteen or eight waves that fit.  Two stages of half as many waves took 2%
   // longer (16 tokens, 256 experts of 7,168 x 2,048).
-  __device__ __forceinline__ void product(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
-                                          const uint32_t (&xso)[NT], int first, int tiles,
-                                          f32x4 (&acc)[TILES][NT]) const {
+  template <int N>
+  __device__ __forceinline__ void product_of(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
+                                             const uint32_t (&xso)[NT], int first,
+                                             f32x4 (&acc)[TILES][NT]) const {
     const bool odd = (x.K / 128) & 1;
-    TokenPair t[NT];
+    TokenPair t[N];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (n < tiles) x.load(first, xo[n], xso[n], t[n]);
+    for (int n = 0; n < N; ++n) x.load(first, xo[n], xso[n], t[n]);
     for (int i = first; i < ring.pairs; i += kWaves) {
       in_order();
       wait_loads<0>();
       in_order();
-      uint32_t xs[NT][2];
+      uint32_t xs[N][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= tiles) continue;
+      for (int n = 0; n < N; ++n) {
         t[n].deal();
         xs[n][0] = t[n].scale(0);
         xs[n][1] = t[n].scale(1);
@@ -295,19 +294,28 @@ struct Shared {
         for (int u = 0; u < 2; ++u) {
           if (u == 1 && !two) break;
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < tiles) acc[m][n] = mma(w[m & 1][u], ws[m & 1][u], t[n].lo[u], t[n].hi[u], xs[n][u], acc[m][n]);
+          for (int n = 0; n < N; ++n)
+            acc[m][n] = mma(w[m & 1][u], ws[m & 1][u], t[n].lo[u], t[n].hi[u], xs[n][u], acc[m][n]);
         }
       }
       in_order();
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n < tiles) x.load(i + kWaves, xo[n], xso[n], t[n]);
+      for (int n = 0; n < N; ++n) x.load(i + kWaves, xo[n], xso[n], t[n]);
       ring.issue_scales(i + kWaves, 0);
     }
     in_order();
     wait_loads<0>();  // the ring is free again
     in_order();
+  }
+  __device__ __forceinline__ void product(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
+                                          const uint32_t (&xso)[NT], int first, int tiles,
+                                          f32x4 (&acc)[TILES][NT]) const {
+    if (NT >= 3 && tiles >= 3)
+      product_of<NT>(ring, x, xo, xso, first, acc);
+    else if (NT >= 2 && tiles >= 2)
+      product_of<NT < 2 ? NT : 2>(ring, x, xo, xso, first, acc);
+    else
+      product_of<1>(ring, x, xo, xso, first, acc);
   }
   // Where a wave's sum of rows 4 j to 4 j + 3 for token r of tokens' tile n
   // lies.  The token's place is turned by j, so that neither neighbouring j of
