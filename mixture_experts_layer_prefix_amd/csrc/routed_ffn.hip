@@ -160,13 +160,19 @@ __device__ __forceinline__ u32x4 of_lane(int from, u32x4 v) {
   return u32x4{of_lane(from, v[0]), of_lane(from, v[1]), of_lane(from, v[2]), of_lane(from, v[3])};
 }
 
-// Sixteen tokens' part of a pair of slabs.  It is loaded with a token's 64
-// bytes in four lanes side by side, which cost the L1 cache one access, and
-// then dealt to the lanes that feed it.
+// Sixteen tokens' part of a pair of slabs.  DEAL: it is loaded with a token's
+// 64 bytes in four lanes side by side, which cost the L1 cache one access, and
+// then dealt to the lanes that feed it; else as it is fed, where the four lanes
+// lie apart and cost four.  Many tokens are bound by these accesses (512 of
+// eight, 32 experts of 7,168 x 2,048: 447 us, dealt 386); where an expert has one
+// or two the others' lanes load nothing, and dealing only delays the product (5
+// tokens, 64 of 2,048 x 768: 21.0 us, dealt 21.6).
+template <bool DEAL>
 struct TokenPair {
   u32x4 lo[2], hi[2];
-  uint32_t xs;  // scales of slab 0 in even lanes, of slab 1 in odd ones
+  uint32_t xs;  // a token's scales of slab 0 in one of its lanes, of slab 1 in the next
   __device__ __forceinline__ void deal() {
+    if constexpr (!DEAL) return;
     const int lane = threadIdx.x & 63, from = (lane & 15) * 16 + (lane >> 4) * 4;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -177,23 +183,26 @@ struct TokenPair {
   // The lane's scale of slab u.
   __device__ __forceinline__ uint32_t scale(int u) const {
     const int lane = threadIdx.x & 63;
-    return of_lane((lane & 15) * 16 + u * 4, xs) >> ((lane >> 4) * 8);
+    return of_lane(DEAL ? (lane & 15) * 16 + u * 4 : (lane & 15) * 4 + u * 64, xs) >> ((lane >> 4) * 8);
   }
 };
 
 // Tokens [][K] in E4M3 and their scales.
+template <bool DEAL>
 struct Tokens {
   Bytes x, xs;
   int K;
-  // Of a lane's loads of token lane / 4.
+  // Which of sixteen tokens a lane loads, and which quarter of its 64 bytes.
+  __device__ static __forceinline__ int token() { return DEAL ? (threadIdx.x & 63) >> 2 : threadIdx.x & 15; }
+  __device__ static __forceinline__ int quarter() { return DEAL ? threadIdx.x & 3 : (threadIdx.x & 63) >> 4; }
   __device__ __forceinline__ uint32_t offset(bool on, uint32_t row) const {
-    return on ? row * K + (threadIdx.x & 3) * 16 : x.n;
+    return on ? row * K + quarter() * 16 : x.n;
   }
   __device__ __forceinline__ uint32_t scale_offset(bool on, uint32_t row) const {
-    return on ? row * (K / 32) + (threadIdx.x & 1) * 4 : xs.n;
+    return on ? row * (K / 32) + quarter() % 2 * 4 : xs.n;
   }
   // Pair i; the second slab of an odd last pair is not used.
-  __device__ __forceinline__ void load(int i, uint32_t o, uint32_t so, TokenPair& t) const {
+  __device__ __forceinline__ void load(int i, uint32_t o, uint32_t so, TokenPair<DEAL>& t) const {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       t.lo[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o, i * 256 + u * 128, 0);
@@ -247,17 +256,17 @@ struct Shared {
   }
 
   // acc[m][n] += the slab pairs first, first + kWaves, ... of 16 * TILES rows
-  // and the first `tiles` (up to NT) times sixteen tokens; the first pair's
-  // weights are under way.  No barrier: the ring is the wave's own.  One pair
-  // of each wave is in flight: 8.5 or 17 KB, 139 KB on a compute unit with the
+  // and N (up to NT) times sixteen tokens; the first pair's weights are under
+  // way.  No barrier: the ring is the wave's own.  One pair of each wave is in
+  // flight, a tile's codes of the next one as soon as the tile's operand is in
+  // registers: 8.5 or 17 KB, 139 KB on a compute unit with the
   // sixteen or eight waves that fit.  Two stages of half as many waves took 2%
   // longer (16 tokens, 256 experts of 7,168 x 2,048).
   template <int N>
-  __device__ __forceinline__ void product_of(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
-                                             const uint32_t (&xso)[NT], int first,
-                                             f32x4 (&acc)[TILES][NT]) const {
+  __device__ __forceinline__ void product_of(const R& ring, const Tokens<!DIRECT>& x, const uint32_t (&xo)[NT],
+                                             const uint32_t (&xso)[NT], int first, f32x4 (&acc)[TILES][NT]) const {
     const bool odd = (x.K / 128) & 1;
-    TokenPair t[N];
+    TokenPair<!DIRECT> t[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) x.load(first, xo[n], xso[n], t[n]);
     for (int i = first; i < ring.pairs; i += kWaves) {
@@ -307,7 +316,9 @@ struct Shared {
     wait_loads<0>();  // the ring is free again
     in_order();
   }
-  __device__ __forceinline__ void product(const R& ring, const Tokens& x, const uint32_t (&xo)[NT],
+  // The first `tiles` times sixteen tokens, NT at most: a product for each
+  // number, without tests between the matrix operations.
+  __device__ __forceinline__ void product(const R& ring, const Tokens<!DIRECT>& x, const uint32_t (&xo)[NT],
                                           const uint32_t (&xso)[NT], int first, int tiles,
                                           f32x4 (&acc)[TILES][NT]) const {
     if (NT >= 3 && tiles >= 3)
@@ -413,13 +424,13 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
   ring.rows(1, p.w.q_up, p.w.q_up_scale, (int64_t)my.e * p.I + c0, p.d);
   ring.issue(wave, 0);  // the first weights are under way while the tokens are found
   if (!my.find(shared)) return;
-  const Tokens x{{p.x, (uint32_t)(p.T * p.d)}, {p.x_scale, (uint32_t)(p.T * (p.d / 32))}, p.d};
+  const Tokens<!DIRECT> x{{p.x, (uint32_t)(p.T * p.d)}, {p.x_scale, (uint32_t)(p.T * (p.d / 32))}, p.d};
   for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
     if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int i = n0 + 16 * n + (threadIdx.x & 63) / 4;
+      const int i = n0 + 16 * n + x.token();
       const bool on = i < my.count;
       const int row = on ? my.row(shared, i) : 0;
       const uint32_t t = !on ? 0 : DIRECT ? row / p.k : row_token[row];
@@ -477,13 +488,13 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
   ring.rows(1, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0 + kCols / 2, p.I);
   ring.issue(wave, 0);
   if (!my.find(shared)) return;
-  const Tokens x{{h, (uint32_t)(p.T * p.k * p.I)}, {h_scale, (uint32_t)(p.T * p.k * (p.I / 32))}, p.I};
+  const Tokens<!DIRECT> x{{h, (uint32_t)(p.T * p.k * p.I)}, {h_scale, (uint32_t)(p.T * p.k * (p.I / 32))}, p.I};
   for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
     if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
     uint32_t xo[NT], xso[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int i = n0 + 16 * n + (threadIdx.x & 63) / 4;
+      const int i = n0 + 16 * n + x.token();
       const bool on = i < my.count;
       const uint32_t row = on ? my.row(shared, i) : 0;
       xo[n] = x.offset(on, row);
