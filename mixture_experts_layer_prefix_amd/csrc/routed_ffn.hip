@@ -11,9 +11,10 @@
 // rows against sixteen tokens.  One token through 8 of 256 experts of 7,168 x
 // 2,048 takes 37 us for 187 MB (5.1 TB/s, two launches; the gate and up
 // projections by themselves 5.4 TB/s), sixteen tokens 391 for 2.4 GB (6.1
-// TB/s).  From a mean of some 40 tokens an expert on the matrix cores' feeding
-// from LDS bounds it instead (512 tokens of eight, 32 experts: 447 us, 0.8
-// PFLOP/s).
+// TB/s).  From a mean of some 40 tokens an expert on the weights, read
+// once for every 48 tokens, and the tokens, read once for every 128 rows, come
+// from L2 with little to hide their way behind (512 tokens of eight, 32 experts:
+// 366 us, 1.0 PFLOP/s).
 #include <algorithm>
 #include <type_traits>
 
@@ -28,9 +29,9 @@ constexpr int kWaves = 4;  // of a workgroup, which share the K of a tile
 // Routes up to which a workgroup finds its expert's tokens by itself, with a
 // workgroup for every route: where there are as many experts as routes, or one
 // tile holds all tokens.  It saves the schedule (8 tokens, one expert of 7,168 x
-// 2,048: 24.4 us, after a schedule 26.0; 4 tokens, 8 of 2,048 x 768, k = 4: 16.1,
-// 20.5), but reads sixteen tokens at a time and starts a workgroup for every
-// route (16 tokens, 8 of 4,096 x 1,536, k = 2: 35.2, after a schedule 28.7).
+// 2,048: 23.6 us, after a schedule 25.7; 4 tokens, 8 of 2,048 x 768, k = 4: 15.8,
+// 20.3), but reads sixteen tokens at a time and starts a workgroup for every
+// route (16 tokens, 8 of 4,096 x 1,536, k = 2: 34.6, after a schedule 28.4).
 constexpr int kDirect = 1024;
 
 // The wave's number in its workgroup, in a scalar register.
@@ -76,7 +77,7 @@ __device__ __forceinline__ void in_order() {
 // the hint 6.3; as sixteen rows of half a line with the hint 5.0), and which
 // hold no registers while they are under way.  Without the hint are weights
 // that several workgroups or rounds read, which are to stay in L2 (512 tokens
-// of eight, 32 experts of 7,168 x 2,048: 447 us, all with the hint 503).  A
+// of eight, 32 experts of 7,168 x 2,048: 366 us, all with the hint 440).  A
 // lane's 16 bytes are put in a place turned by its row, so that the reads of
 // sixteen rows of a slab meet no bank twice.  Scales: a word per row and slab.
 template <int TILES, int STAGES>
@@ -164,9 +165,9 @@ __device__ __forceinline__ u32x4 of_lane(int from, u32x4 v) {
 // 64 bytes in four lanes side by side, which cost the L1 cache one access, and
 // then dealt to the lanes that feed it; else as it is fed, where the four lanes
 // lie apart and cost four.  Many tokens are bound by these accesses (512 of
-// eight, 32 experts of 7,168 x 2,048: 447 us, dealt 386); where an expert has one
+// eight, 32 experts of 7,168 x 2,048: 446 us, dealt 366); where an expert has one
 // or two the others' lanes load nothing, and dealing only delays the product (5
-// tokens, 64 of 2,048 x 768: 21.0 us, dealt 21.6).
+// tokens, 64 of 2,048 x 768: 21.0 us, dealt 21.5).
 template <bool DEAL>
 struct TokenPair {
   u32x4 lo[2], hi[2];
@@ -520,8 +521,8 @@ __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t
 
 constexpr int kDownWaves = 8;
 // Two stages let four workgroups onto a compute unit (four stages two of them,
-// with as much in flight: 4 tokens, 256 experts of 7,168 x 2,048, 121.8 us, with
-// two 114.2; 5 tokens, 64 of 2,048 x 768, 24.0, 21.0).
+// with as much in flight: 4 tokens, 256 experts of 7,168 x 2,048, 120.4 us, with
+// two 113.4; 5 tokens, 64 of 2,048 x 768, 23.9, 21.1).
 constexpr int kTokenStages = 2;
 
 // A token's sixteen columns of y, h with a row per route: each wave takes the
@@ -685,25 +686,25 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
 // that chose it: R^2 / 2E experts for R routes at random, weighed here in
 // weights.  us of the whole call, by token and by expert (tokens, experts of d x
 // I, k):
-//   1, 256 of 7,168 x 2,048, 8    38.3  -        2, 64 of 2,048 x 768, 6    16.2  21.3
-//   2                             63.0  69.0     5                          20.9  25.0
-//   4                             114.0 119.3    10                         34.8  37.1
-//   8                             211.9 214.1    4, 128 of 4,096 x 1,536, 8 55.7  60.8
-//   16                            392.4 390.5    8                          97.0  97.9
+//   1, 256 of 7,168 x 2,048, 8    38.2  -        2, 64 of 2,048 x 768, 6    16.1  21.0
+//   2                             62.4  68.2     5                          20.7  24.7
+//   4                             113.7 117.8    10                         34.5  36.7
+//   8                             210.3 211.5    4, 128 of 4,096 x 1,536, 8 55.3  59.9
+//   16                            393.4 390.4    8                          96.5  97.1
 constexpr int64_t kRepeats = 500000000;
 
 // Which tiles, after the schedule.  An expert's tokens are shared by as many
-// workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 306
-// us with one, 73 with sixteen).
+// workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 220
+// us with one, 59 with eleven).
 //   128 weight rows against 48 tokens, from a mean of 24 tokens an expert on:
 //     most experts' tokens are then together and their weights read once (32
-//     experts of 7,168 x 2,048, 128 tokens of eight: 182 us, with 32 tokens at a
-//     time 230; 96 tokens 165 and 161).
+//     experts of 7,168 x 2,048, 128 tokens of eight: 165 us, with 32 tokens at a
+//     time 215; 96 tokens 151 and 149).
 //   128 against 32: each token read half as often as by 64 rows (333 tokens, 128
-//     experts of 4,096 x 1,536: 273 us, 307).
+//     experts of 4,096 x 1,536: 260 us, 280).
 //   64 against 32 where workgroups are few, for twice as many (64 tokens, one
-//     expert of 7,168 x 2,048: 31.6 us, by 128 rows 39.2; 16 tokens, 8 of 4,096 x
-//     1,536: 29.0, 30.5).
+//     expert of 7,168 x 2,048: 27.3 us, by 128 rows 32.2; 16 tokens, 8 of 4,096 x
+//     1,536: 28.6, 30.3).
 constexpr int64_t kManyTokens = 24, kFewGroups = 512;
 
 hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
