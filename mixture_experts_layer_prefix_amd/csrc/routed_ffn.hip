@@ -227,6 +227,16 @@ struct Shared {
 
   __device__ __forceinline__ uint8_t* wave(int w) { return bytes + w * kWave; }
 
+  // The same by each wave for itself, without a barrier, for up to 64 routes;
+  // id: the lane's.  The wave's list begins at 64 * wave.
+  __device__ __forceinline__ int find_few(int32_t id, int e, int mine) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t m = __ballot(id == e), before = (1ull << lane) - 1;
+    if (m & ((1ull << mine) - 1)) return 0;
+    if ((m >> lane) & 1) list[64 * wave_id() + __popcll(m & before)] = lane;
+    in_order();
+    return __popcll(m);
+  }
   // The routes of expert e, in order, into `list`; id: the thread's ids of the
   // routes threadIdx.x, 256 + threadIdx.x, ...  Their number, or 0 if one comes
   // before route `mine`.
@@ -363,6 +373,7 @@ struct Served {
   int e, first, count;
   int tile, part, parts;  // of the columns; of the tokens, and how many there are
   int32_t id[kDirect / 256];
+  bool few;                 // routes: each wave finds them by itself
 
   // False: there is nothing to do.
   __device__ __forceinline__ bool begin(const RoutedFfn& p, const int32_t* offsets, int tiles) {
@@ -373,11 +384,13 @@ struct Served {
       e = p.topk_idx[blockIdx.y];
       first = 0;
       count = 1;  // at least, until find()
+      const int routes = (int)p.T * p.k;
+      few = routes <= 64;
       if ((unsigned)e >= (unsigned)p.E) return false;
 #pragma unroll
       for (int q = 0; q < kDirect / 256; ++q) {
-        const int i = q * 256 + (int)threadIdx.x;
-        id[q] = i < (int)p.T * p.k ? p.topk_idx[i] : -1;
+        const int i = q * 256 + (few ? (int)threadIdx.x & 63 : (int)threadIdx.x);
+        id[q] = i < routes ? p.topk_idx[i] : -1;
       }
       in_order();  // waited for behind the first weights, these would wait for them too
       return true;
@@ -397,14 +410,15 @@ struct Served {
   template <class S>
   __device__ __forceinline__ bool find(S& shared) {
     if constexpr (DIRECT) {
-      count = shared.find(id, e, blockIdx.y);
+      count = few ? shared.find_few(id[0], e, blockIdx.y) : shared.find(id, e, blockIdx.y);
+      if (few) first = 64 * wave_id();
       if (count == 0) wait_loads<0>();  // no load may reach LDS that is another workgroup's by then
     }
     return count > 0;
   }
   template <class S>
   __device__ __forceinline__ int row(const S& shared, int i) const {
-    return DIRECT ? shared.list[i] : first + i;
+    return DIRECT ? shared.list[first + i] : first + i;
   }
 };
 
