@@ -26,12 +26,7 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 4;  // of a workgroup, which share the K of a tile
-// Routes up to which a workgroup finds its expert's tokens by itself, with a
-// workgroup for every route: where there are as many experts as routes, or one
-// tile holds all tokens.  It saves the schedule (8 tokens, one expert of 7,168 x
-// 2,048: 23.6 us, after a schedule 25.7; 4 tokens, 8 of 2,048 x 768, k = 4: 15.8,
-// 20.3), but reads sixteen tokens at a time and starts a workgroup for every
-// route (16 tokens, 8 of 4,096 x 1,536, k = 2: 34.6, after a schedule 28.4).
+// Routes that a workgroup can look through for its expert's tokens.
 constexpr int kDirect = 1024;
 
 // The wave's number in its workgroup, in a scalar register.
@@ -368,7 +363,7 @@ struct Shared {
 // (., i) serves the expert of route i if no earlier route has it, and finds the
 // others by reading all ids; h and o have a row per route.  Else workgroup
 // (., e) serves expert e after the sort's schedule, whose rows h and o have.
-template <bool DIRECT>
+template <bool DIRECT, bool ALONE>
 struct Served {
   int e, first, count;
   int tile, part, parts;  // of the columns; of the tokens, and how many there are
@@ -385,7 +380,7 @@ struct Served {
       first = 0;
       count = 1;  // at least, until find()
       const int routes = (int)p.T * p.k;
-      few = routes <= 64;
+      few = ALONE || routes <= 64;
       if ((unsigned)e >= (unsigned)p.E) return false;
 #pragma unroll
       for (int q = 0; q < kDirect / 256; ++q) {
@@ -407,10 +402,28 @@ struct Served {
       return true;
     }
   }
+  // The first weights are under way while the tokens are found; but not where
+  // many workgroups find that they have none (16 tokens, 256 experts of 7,168 x
+  // 2,048, k = 8: 380.5 us, always early 389; 2 tokens, 64 of 2,048 x 768, k = 6:
+  // 15.8, early 15.1).
+  template <class S, class Issue>
+  __device__ __forceinline__ bool start(S& shared, Issue issue) {
+    if constexpr (!DIRECT || ALONE) {
+      issue();
+      return find(shared);
+    } else {
+      if (!find(shared)) return false;
+      issue();
+      return true;
+    }
+  }
   template <class S>
   __device__ __forceinline__ bool find(S& shared) {
     if constexpr (DIRECT) {
-      count = few ? shared.find_few(id[0], e, blockIdx.y) : shared.find(id, e, blockIdx.y);
+      if (ALONE || few)
+        count = shared.find_few(id[0], e, blockIdx.y);
+      else
+        count = shared.find(id, e, blockIdx.y);
       if (few) first = 64 * wave_id();
       if (count == 0) wait_loads<0>();  // no load may reach LDS that is another workgroup's by then
     }
@@ -423,22 +436,21 @@ struct Served {
 };
 
 // 8 * TILES columns of h for an expert's tokens.
-template <int TILES, int NT, bool DIRECT>
+template <int TILES, int NT, bool DIRECT, bool ALONE>
 __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
                                                          const int32_t* __restrict__ row_token,
                                                          uint8_t* __restrict__ h, uint8_t* __restrict__ h_scale) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 8 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
   const int lane = threadIdx.x & 63, wave = wave_id();
-  Served<DIRECT> my;
+  Served<DIRECT, ALONE> my;
   if (!my.begin(p, offsets, p.I / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
   ring.begin(shared.wave(wave), p.d, (int64_t)p.E * p.I, !DIRECT && my.count > 16 * NT);
   ring.rows(0, p.w.q_gate, p.w.q_gate_scale, (int64_t)my.e * p.I + c0, p.d);
   ring.rows(1, p.w.q_up, p.w.q_up_scale, (int64_t)my.e * p.I + c0, p.d);
-  ring.issue(wave, 0);  // the first weights are under way while the tokens are found
-  if (!my.find(shared)) return;
+  if (!my.start(shared, [&] { ring.issue(wave, 0); })) return;
   const Tokens<!DIRECT> x{{p.x, (uint32_t)(p.T * p.d)}, {p.x_scale, (uint32_t)(p.T * (p.d / 32))}, p.d};
   for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
     if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
@@ -487,22 +499,21 @@ __global__ void __launch_bounds__(256, 2) gate_up_kernel(RoutedFfn p, const int3
 }
 
 // 16 * TILES columns of o for an expert's tokens.
-template <int TILES, int NT, bool DIRECT>
+template <int TILES, int NT, bool DIRECT, bool ALONE>
 __global__ void __launch_bounds__(256, 2) down_kernel(RoutedFfn p, const int32_t* __restrict__ offsets,
                                                       const uint8_t* h, const uint8_t* h_scale,
                                                       float* __restrict__ o) {
   __shared__ Shared<TILES, NT, DIRECT> shared;
   constexpr int kCols = 16 * TILES, kAtOnce = Shared<TILES, NT, DIRECT>::kAtOnce;
   const int wave = wave_id();
-  Served<DIRECT> my;
+  Served<DIRECT, ALONE> my;
   if (!my.begin(p, offsets, p.d / kCols) || my.part * 16 * NT >= my.count) return;
   const int c0 = my.tile * kCols;
   Ring<TILES, 1> ring;
   ring.begin(shared.wave(wave), p.I, (int64_t)p.E * p.d, !DIRECT && my.count > 16 * NT);
   ring.rows(0, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0, p.I);
   ring.rows(1, p.w.q_down, p.w.q_down_scale, (int64_t)my.e * p.d + c0 + kCols / 2, p.I);
-  ring.issue(wave, 0);
-  if (!my.find(shared)) return;
+  if (!my.start(shared, [&] { ring.issue(wave, 0); })) return;
   const Tokens<!DIRECT> x{{h, (uint32_t)(p.T * p.k * p.I)}, {h_scale, (uint32_t)(p.T * p.k * (p.I / 32))}, p.I};
   for (int n0 = my.part * 16 * NT; n0 < my.count; n0 += my.parts * 16 * NT) {
     if (n0 > my.part * 16 * NT) ring.issue(wave, 0);
@@ -695,17 +706,29 @@ size_t routed_ffn_scratch_bytes(int64_t T, int d, int E, int k, int I) {
   return carve(nullptr, T, d, E, k, I).bytes;
 }
 
-// Which down projection.  By token it needs no sum of its own, which saves a
-// launch and o's way through memory, but reads an expert anew for every token
-// that chose it: R^2 / 2E experts for R routes at random, weighed here in
-// weights.  us of the whole call, by token and by expert (tokens, experts of d x
-// I, k):
-//   1, 256 of 7,168 x 2,048, 8    38.2  -        2, 64 of 2,048 x 768, 6    16.1  21.0
-//   2                             62.4  68.2     5                          20.7  24.7
-//   4                             113.7 117.8    10                         34.5  36.7
-//   8                             210.3 211.5    4, 128 of 4,096 x 1,536, 8 55.3  59.9
-//   16                            393.4 390.4    8                          96.5  97.1
-constexpr int64_t kRepeats = 500000000;
+// With or without a schedule.  Without one there is a workgroup for every route,
+// which finds its expert's tokens by itself, sixteen at a time, or that an earlier
+// route has the expert: some R^2 / 2E of R at random, weighed here by the
+// workgroups of a route.  us (tokens, experts of d x I, k: without, with):
+//   1, 8 of 256 of 7,168 x 2,048    37.0 -      10, 64 of 2,048 x 768, 6   31.6  39.2
+//   8, 256, 8                      205.6 220.3  14                         41.1  44.5
+//   16                             380.9 377.2  20                         48.2  46.3
+//   12, 8 of 4,096 x 1,536, 2       29.7 28.1   16, 8 of 2,048 x 768, 2    18.1  20.9
+// Up to sixteen routes are one tile of tokens whatever they share, and the
+// schedule is never worth its launches (16 tokens, one expert of 7,168 x 2,048:
+// 22.9, 26.5).
+constexpr int64_t kTwice = 500000;
+
+// Which down projection, without a schedule.  By token it needs no sum of its
+// own, which saves a launch and o's way through memory, but reads an expert anew
+// for every token that chose it, weighed here in weights, and a token's routes
+// are its waves (one route: 32 tokens, 64 experts of 2,048 x 768, 25.9, by expert
+// 22.3).  us (tokens, experts of d x I, k: by token, by expert):
+//   2, 256 of 7,168 x 2,048, 8      62.3 68.0   10, 64 of 2,048 x 768, 6   31.6  31.8
+//   4                              112.1 115.6  14                         41.1  42.7
+//   8                              208.2 205.6  6, 16 of 4,096 x 1,536, 4  35.5  33.5
+//   8, 128 of 4,096 x 1,536, 8      92.5 90.3   32, 512 of 2,048 x 512, 8  86.8  90.6
+constexpr int64_t kRepeats = 200000000;
 
 // Which tiles, after the schedule.  An expert's tokens are shared by as many
 // workgroups as the mean calls for (512 tokens, one expert of 7,168 x 2,048: 220
@@ -725,15 +748,18 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   const Scratch b = carve(static_cast<char*>(scratch), p.T, p.d, p.E, p.k, p.I);
   const int64_t R = p.T * p.k, steps = p.T * ceil_div(p.d, 1024);
   const unsigned sums = (unsigned)(steps < 65536 ? steps : 65536);
-  if (R <= kDirect && (R <= p.E || R <= 16)) {
+  if (R <= 16 || (R <= kDirect && R * R * (2 * p.I + p.d) / p.E <= kTwice)) {
     const unsigned routes = (unsigned)R;
-    gate_up_kernel<4, 1, true><<<dim3(p.I / 32, routes), 256, 0, s>>>(p, nullptr, nullptr, b.h, b.h_scale);
-    if (p.T == 1 || R * R * p.I * p.d / p.E <= kRepeats) {
+    const bool alone = R <= 16 && R <= p.E;  // hardly a route shares its expert
+    const auto gate_up = alone ? gate_up_kernel<4, 1, true, true> : gate_up_kernel<4, 1, true, false>;
+    gate_up<<<dim3(p.I / 32, routes), 256, 0, s>>>(p, nullptr, nullptr, b.h, b.h_scale);
+    if (p.T == 1 || (p.k > 1 && R * R * p.I * p.d / p.E <= kRepeats)) {
       const int waves = p.k < kDownWaves ? p.k : kDownWaves;
       down_token_kernel<<<(unsigned)(p.T * (p.d / 16)), 64 * waves, 0, s>>>(p, b.h, b.h_scale);
       return hipGetLastError();
     }
-    down_kernel<4, 1, true><<<dim3(p.d / 64, routes), 256, 0, s>>>(p, nullptr, b.h, b.h_scale, b.o);
+    const auto down = alone ? down_kernel<4, 1, true, true> : down_kernel<4, 1, true, false>;
+    down<<<dim3(p.d / 64, routes), 256, 0, s>>>(p, nullptr, b.h, b.h_scale, b.o);
     weighted_sum_kernel<true><<<sums, 256, 0, s>>>(p, nullptr, b.o);
     return hipGetLastError();
   }
@@ -748,9 +774,9 @@ hipError_t launch_routed_ffn(const RoutedFfn& p, void* scratch, hipStream_t s) {
   auto run = [&](auto TILES, auto NT) {
     constexpr int t = TILES.value, nt = NT.value;
     const int64_t n = parts(nt);
-    gate_up_kernel<t, nt, false><<<dim3((unsigned)(p.I / (8 * t) * n), (unsigned)p.E), 256, 0, s>>>(
+    gate_up_kernel<t, nt, false, false><<<dim3((unsigned)(p.I / (8 * t) * n), (unsigned)p.E), 256, 0, s>>>(
         p, b.offsets, b.row_token, b.h, b.h_scale);
-    down_kernel<t, nt, false><<<dim3((unsigned)(p.d / (16 * t) * n), (unsigned)p.E), 256, 0, s>>>(
+    down_kernel<t, nt, false, false><<<dim3((unsigned)(p.d / (16 * t) * n), (unsigned)p.E), 256, 0, s>>>(
         p, b.offsets, b.h, b.h_scale, b.o);
   };
   constexpr std::integral_constant<int, 2> two;

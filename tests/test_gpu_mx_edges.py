@@ -97,6 +97,20 @@ def test_routed_ffn_every_token_at_one_expert(T, d, E, k, I):
     assert np.all(off <= bound), (off / bound).max()
 
 
+def test_routed_ffn_128_routes_by_expert():
+    """Without a schedule, found by whole workgroups, down by expert."""
+    T, d, E, k, I = 16, 1280, 130, 8, 1280
+    x, xs, w = real_problem(17, T, d, E, k, I)
+    idx, tw = ids(5, T, k, 0, E), torch.rand(T, k, generator=gen(2), device="cuda")
+    idx[3] = idx[2]
+    idx[7, 2:5] = -1
+    y = poisoned(M.Dims(T, d, E, k, I)).run(x, xs, idx, tw, w)
+    one = M.RoutedFfnPlan(M.Dims(1, d, E, k, I))
+    for t in range(T):
+        s = slice(t, t + 1)
+        assert torch.equal(one.run(x[s], xs[s], idx[s], tw[s], w), y[s]), t
+
+
 def test_routed_ffn_one_expert_by_expert():
     T, d, E, k, I = 512, 1024, 512, 1, 1024
     x, xs, w = real_problem(13, T, d, E, k, I)
