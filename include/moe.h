@@ -582,8 +582,8 @@ typedef struct {
  * MOE_EUNSUPPORTED);
  * 1 <= E <= 1024, 1 <= k <= 16 (k may exceed E).  Any T is computed; from
  * about 300 routes an expert on sort, moe_expert_ffn in MOE_MXFP8 and unsort
- * are faster (32 experts of 7,168 x 2,048, 256 routes each: 627 us, those 620;
- * 512 routes: 1,133, 1,013).  ws: moe_workspace_bytes(which = 6) bytes. */
+ * are faster (32 experts of 7,168 x 2,048, 256 routes each: 626 us, those 620
+ * to 658; 512 routes: 1,136, 979 to 1,013).  ws: moe_workspace_bytes(which = 6) bytes. */
 moe_status moe_routed_ffn_mxfp4(const moe_dims* dims, const uint8_t* x, const uint8_t* x_scale,
                                 const int32_t* topk_idx, const float* topk_w, const moe_weights_mxfp4* w,
                                 const void* y_add, void* y, void* ws, size_t ws_bytes, void* stream);

@@ -9,8 +9,8 @@
 // matrix cores: v_mfma_scale_f32_16x16x128_f8f6f4 takes E2M1 weights and E4M3
 // activations with their block scales as they lie in memory, sixteen weight
 // rows against sixteen tokens.  One token through 8 of 256 experts of 7,168 x
-// 2,048 takes 37 us for 187 MB (5.1 TB/s, two launches; the gate and up
-// projections by themselves 5.4 TB/s), sixteen tokens 391 for 2.4 GB (6.1
+// 2,048 takes 36 us for 187 MB (5.3 TB/s, two launches; the gate and up
+// projections by themselves 5.7 TB/s), sixteen tokens 377 for 2.4 GB (6.3
 // TB/s).  From a mean of some 40 tokens an expert on the weights, read
 // once for every 48 tokens, and the tokens, read once for every 128 rows, come
 // from L2 with little to hide their way behind (512 tokens of eight, 32 experts:
@@ -361,7 +361,8 @@ struct Shared {
 
 // Which rows of a matrix a tile kernel's workgroup serves.  DIRECT: workgroup
 // (., i) serves the expert of route i if no earlier route has it, and finds the
-// others by reading all ids; h and o have a row per route.  Else workgroup
+// others by reading all ids; h and o have a row per route.  ALONE: sixteen
+// routes at most, of which hardly any shares its expert.  Else workgroup
 // (., e) serves expert e after the sort's schedule, whose rows h and o have.
 template <bool DIRECT, bool ALONE>
 struct Served {
