@@ -42,9 +42,8 @@ def test_routed_ffn_variants_whole_numbers(T, d, E, k, I, lo, hi):
 
 
 def test_routed_ffn_many_experts_by_expert():
-    """Few routes whose repeated experts outweigh a sum of its own: the down
-    projection goes by expert without a schedule.  Bits of a token alone, and
-    a token's numbers."""
+    """As many routes as experts, whose shared experts outweigh a schedule.
+    Bits of a token alone, and a token's numbers."""
     T, d, E, k, I = 64, 1024, 512, 8, 1024
     x, xs, w = real_problem(11, T, d, E, k, I)
     idx, tw = ids(5, T, k, 0, E), torch.rand(T, k, generator=gen(2), device="cuda")
@@ -111,7 +110,7 @@ def test_routed_ffn_128_routes_by_expert():
         assert torch.equal(one.run(x[s], xs[s], idx[s], tw[s], w), y[s]), t
 
 
-def test_routed_ffn_one_expert_by_expert():
+def test_routed_ffn_nearly_every_token_at_one_expert():
     T, d, E, k, I = 512, 1024, 512, 1, 1024
     x, xs, w = real_problem(13, T, d, E, k, I)
     idx = torch.full((T, k), 77, dtype=I32, device="cuda")
