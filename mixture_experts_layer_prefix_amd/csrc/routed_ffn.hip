@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "mxfp4.h"
+#include "parts.h"
 #include "rows.h"
 
 namespace moe {
@@ -43,7 +44,8 @@ __device__ __forceinline__ f32x4 mma(u32x4 w, uint32_t ws, u32x4 lo, u32x4 hi, u
 }
 
 // Bytes that are read through a buffer address: reads at or past the end (the
-// sum of a scalar and a lane's offset) give zeros and cost no traffic.
+// sum of a scalar and a lane's offset) give zeros and cost no traffic.  The
+// scalar offset alone never passes the end (part_at()).
 struct Bytes {
   const uint8_t* p;
   uint32_t n;
@@ -88,14 +90,15 @@ struct Ring {
   uint32_t even, odd, scale;       // a lane's offsets in eight rows' codes, and in the scales
   uint32_t ld, ws_step;            // bytes of eight rows' codes, between slabs of scales
   uint32_t read, read_scale;       // a lane's place in a stage
-  int pairs;
+  int pairs, slabs;
   bool again;                      // the weights are read more than once
 
   __device__ __forceinline__ void begin(uint8_t* ring, int K, int64_t all_rows, bool reread) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
     lds = ring;
     again = reread;
-    pairs = (K + 255) / 256;
+    slabs = K / 128;
+    pairs = (slabs + 1) / 2;
     ld = 4 * K;
     ws_step = (uint32_t)all_rows * 4;
     even = (lane >> 3) * (K / 2) + ((lane & 7) ^ g) * 16;
@@ -112,8 +115,9 @@ struct Ring {
   template <int AUX>
   __device__ __forceinline__ void issue_tile(int i, int t, uint8_t* to) const {
     const int m = t / (TILES / kMats), q = t % (TILES / kMats) * 2;
-    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048, even, i < pairs ? i * 128 + q * ld : w[m].n);
-    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048 + 1024, odd, i < pairs ? i * 128 + (q + 1) * ld : w[m].n);
+    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048, even, part_at(i, pairs, i * 128 + q * ld, w[m].n));
+    lds_dma<16, AUX>(w[m].rsrc(), to + t * 2048 + 1024, odd,
+                     part_at(i, pairs, i * 128 + (q + 1) * ld, w[m].n));
   }
   // Starts the loads of pair i into its stage, whole or in parts: the codes of
   // tile t, the scales.  Past the last pair they read nothing.
@@ -136,7 +140,7 @@ struct Ring {
 #pragma unroll
       for (int v = 0; v < kScaleLoads; ++v)
         lds_dma<4>(ws[m].rsrc(), to + kCodes + (m * kScaleLoads + v) * 256, scale,
-                   i < pairs ? (2 * i + v) * ws_step : ws[m].n);
+                   part_at(2 * i + v, slabs, (2 * i + v) * ws_step, ws[m].n));
   }
   // Tile m's operand and scale of the stage's slab u.
   __device__ __forceinline__ u32x4 codes(int stage, int m, int u) const {
@@ -197,14 +201,17 @@ struct Tokens {
   __device__ __forceinline__ uint32_t scale_offset(bool on, uint32_t row) const {
     return on ? row * (K / 32) + quarter() % 2 * 4 : xs.n;
   }
-  // Pair i; the second slab of an odd last pair is not used.
+  // Pair i; past the last pair nothing is read.  The second slab of an odd last
+  // pair is not used.
   __device__ __forceinline__ void load(int i, uint32_t o, uint32_t so, TokenPair<DEAL>& t) const {
+    const int pairs = (K + 255) / 256;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      t.lo[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o, i * 256 + u * 128, 0);
-      t.hi[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o + 64, i * 256 + u * 128, 0);
+      const uint32_t at = part_at(i, pairs, i * 256 + u * 128, x.n);
+      t.lo[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o, at, 0);
+      t.hi[u] = __builtin_amdgcn_raw_buffer_load_b128(x.rsrc(), o + 64, at, 0);
     }
-    t.xs = __builtin_amdgcn_raw_buffer_load_b32(xs.rsrc(), so, i * 8, 0);
+    t.xs = __builtin_amdgcn_raw_buffer_load_b32(xs.rsrc(), so, part_at(i, pairs, i * 8, xs.n), 0);
   }
 };
 
@@ -583,8 +590,8 @@ __global__ void __launch_bounds__(64 * kDownWaves, 4) down_token_kernel(RoutedFf
     auto issue = [&](int i, int u) {
       uint8_t* to = lds + kRing + u * kToken;
       ring.issue(i, u);
-      if (lane < 16) lds_dma<16>(x.rsrc(), to, lane * 16, i * 256);
-      if (lane < 2) lds_dma<4>(xs.rsrc(), to + 256, lane * 4, i * 8);
+      if (lane < 16) lds_dma<16>(x.rsrc(), to, lane * 16, part_at(i, ring.pairs, i * 256, x.n));
+      if (lane < 2) lds_dma<4>(xs.rsrc(), to + 256, lane * 4, part_at(i, ring.pairs, i * 8, xs.n));
     };
     f32x4 acc[kWaves] = {};
     auto multiply = [&](int u, int stage, int slab) {
