@@ -386,6 +386,21 @@ moe_status moe_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint
  * a or b not 16-byte aligned. */
 moe_status moe_bf16_mma_tiles(const void* a, const void* b, const float* c, float* d, int64_t n, void* stream);
 
+/* Loads through a buffer address of `length` bytes from src on, so that the
+ * address check by which the routed experts' kernels end their reads can be
+ * tested: lane l in [0, lanes) reads 16 bytes at scalar + first + 16 l (scalar
+ * the offset that all lanes share, first + 16 l the lane's) in four forms.  dst,
+ * in words: [lanes][4] loaded into registers, [lanes][4] loaded directly to LDS,
+ * [lanes] the first word by itself into a register, [lanes] that to LDS.  What
+ * lies at `length` or beyond is expected to read as zeros.  src holds `bytes`
+ * bytes, all of which the largest address must lie in whatever the check does:
+ * EINVAL where scalar + first + 16 lanes or length passes them or the lanes'
+ * offsets pass 32 bits, for lanes not a multiple of 64 in [0, 2^24], offsets or
+ * a length that are not multiples of 16, a null pointer, or one not 16-byte
+ * aligned. */
+moe_status moe_buffer_reads(const uint8_t* src, int64_t bytes, uint32_t length, uint32_t scalar, uint32_t first,
+                            int64_t lanes, uint32_t* dst, void* stream);
+
 /* ---- Routed tokens sorted by expert and back, with absent routes ----------
  * moe_permute and moe_combine for callers whose routes may be absent, with
  * the gradients of both: a route whose expert id lies outside [0, E) is

@@ -973,4 +973,15 @@ moe_status moe_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint
   return MOE_OK;
 }
 
+moe_status moe_buffer_reads(const uint8_t* src, int64_t bytes, uint32_t length, uint32_t scalar, uint32_t first,
+                            int64_t lanes, uint32_t* dst, void* stream) {
+  if (lanes < 0 || lanes % 64 || lanes > (1 << 24) || bytes < 0) return MOE_EINVAL;
+  const int64_t past = (int64_t)first + 16 * lanes;  // of the lanes' offsets
+  if (past > UINT32_MAX || (int64_t)scalar + past > bytes || length > bytes) return MOE_EINVAL;
+  if (lanes == 0) return MOE_OK;
+  if (!ptr_ok(src) || !ptr_ok(dst) || first % 16 || scalar % 16 || length % 16) return MOE_EINVAL;
+  MOE_HIP(launch_buffer_reads(src, length, scalar, first, lanes, dst, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
 }  // extern "C"

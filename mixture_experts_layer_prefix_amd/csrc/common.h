@@ -377,5 +377,8 @@ hipError_t launch_bf16_mma_tiles(const bf16_t* a, const bf16_t* b, const float* 
 // One scaled MFMA per tile (moe_mx_mma_tiles).
 hipError_t launch_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
                                const float* c, float* d, int64_t n, hipStream_t s);
+// Loads through a buffer address (moe_buffer_reads); lanes a multiple of 64.
+hipError_t launch_buffer_reads(const uint8_t* src, uint32_t length, uint32_t scalar, uint32_t first, int64_t lanes,
+                               uint32_t* dst, hipStream_t s);
 
 }  // namespace moe

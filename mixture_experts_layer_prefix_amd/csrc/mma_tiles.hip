@@ -16,6 +16,9 @@
 //
 // In both, accumulator element v of lane l is row 4g + 8(v/4) + v%4, column
 // r of the 32x32 result.
+//
+// Beside them the address check of loads through a buffer address, on which
+// csrc/routed_ffn.hip relies to end its reads.
 #include "common.h"
 
 namespace moe {
@@ -64,7 +67,36 @@ __global__ __launch_bounds__(64) void bf16_mma_tiles_kernel(const bf16_t* __rest
   for (int v = 0; v < 16; ++v) dt[(8 * (v >> 2) + (v & 3)) * 32] = acc[v];
 }
 
+// Lane l of all lanes reads 16 bytes at `scalar` + `first` + 16 l of a buffer of
+// `length` bytes in each form that the kernels use: into a register, directly to
+// LDS, and of 4 bytes into a register and to LDS.
+__global__ __launch_bounds__(64) void buffer_reads_kernel(const uint8_t* src, uint32_t length, uint32_t scalar,
+                                                          uint32_t first, int64_t lanes, uint32_t* __restrict__ dst) {
+  __shared__ u32x4 wide[64];
+  __shared__ uint32_t word[64];
+  const int64_t l = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  const uint32_t at = first + 16 * (uint32_t)l;
+  const __amdgpu_buffer_rsrc_t rsrc =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src), 0, (int)length, 0x00027000);
+  lds_dma<16>(rsrc, wide, at, scalar);
+  lds_dma<4>(rsrc, word, at, scalar);
+  const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at, scalar, 0);
+  const uint32_t w = __builtin_amdgcn_raw_buffer_load_b32(rsrc, at, scalar, 0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  *reinterpret_cast<u32x4*>(dst + 4 * l) = v;
+  *reinterpret_cast<u32x4*>(dst + 4 * (lanes + l)) = wide[threadIdx.x];
+  dst[8 * lanes + l] = w;
+  dst[9 * lanes + l] = word[threadIdx.x];
+}
+
 }  // namespace
+
+hipError_t launch_buffer_reads(const uint8_t* src, uint32_t length, uint32_t scalar, uint32_t first, int64_t lanes,
+                               uint32_t* dst, hipStream_t s) {
+  buffer_reads_kernel<<<(unsigned)(lanes / 64), 64, 0, s>>>(src, length, scalar, first, lanes, dst);
+  return hipGetLastError();
+}
 
 hipError_t launch_bf16_mma_tiles(const bf16_t* a, const bf16_t* b, const float* c, float* d, int64_t n,
                                  hipStream_t s) {

@@ -296,6 +296,16 @@ def bf16_mma_tiles(a, b, c):
     return d
 
 
+def buffer_reads(src, length, scalar, first, lanes):
+    """moe_buffer_reads of the uint8 tensor src: int32 (registers [lanes][4],
+    LDS [lanes][4], words in registers [lanes], words in LDS [lanes])."""
+    assert src.dtype == torch.uint8 and src.is_contiguous()
+    dst = torch.empty(10 * lanes, dtype=torch.int32, device=src.device)
+    call("moe_buffer_reads", _p(src), src.numel(), length, scalar, first, lanes, _p(dst), _stream())
+    wide, to_lds, words = dst[:4 * lanes], dst[4 * lanes:8 * lanes], dst[8 * lanes:]
+    return wide.view(lanes, 4), to_lds.view(lanes, 4), words[:lanes], words[lanes:]
+
+
 def prepare_mxfp8(weights: Weights, dims: Dims) -> Weights:
     """Weights with the routed experts pre-quantized for MOE_MXFP8 (blocks
     along each GEMM's K: d for gate/up, I for down)."""
