@@ -110,6 +110,7 @@ _SIGS = {
     "moe_dequantize_mxfp4": ([_P, _P, ctypes.c_int64, ctypes.c_int64, _P, _P], ctypes.c_int),
     "moe_routed_ffn_mxfp4": ([_DIMS] + [_P] * 4 + [ctypes.POINTER(moe_weights_mxfp4)] + [_P] * 3 +
                              [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_mxfp4_mma_tiles": ([_P] * 6 + [ctypes.c_int64, _P], ctypes.c_int),
     "moe_buffer_reads": ([_P, ctypes.c_int64] + [ctypes.c_uint32] * 3 + [ctypes.c_int64, _P, _P], ctypes.c_int),
     "moe_bf16_mma_tiles": ([_P, _P, _P, _P, ctypes.c_int64, _P], ctypes.c_int),
 }

@@ -973,6 +973,15 @@ moe_status moe_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint
   return MOE_OK;
 }
 
+moe_status moe_mxfp4_mma_tiles(const uint8_t* w, const uint8_t* w_scale, const uint8_t* x, const uint8_t* x_scale,
+                               const float* c, float* d, int64_t n, void* stream) {
+  if (n < 0 || n > INT32_MAX) return MOE_EINVAL;
+  if (n == 0) return MOE_OK;
+  if (!ptr_ok(w) || !ptr_ok(x) || !w_scale || !x_scale || !c || !d) return MOE_EINVAL;
+  MOE_HIP(launch_mxfp4_mma_tiles(w, w_scale, x, x_scale, c, d, n, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
 moe_status moe_buffer_reads(const uint8_t* src, int64_t bytes, uint32_t length, uint32_t scalar, uint32_t first,
                             int64_t lanes, uint32_t* dst, void* stream) {
   if (lanes < 0 || lanes % 64 || lanes > (1 << 24) || bytes < 0) return MOE_EINVAL;

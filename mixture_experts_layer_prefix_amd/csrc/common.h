@@ -377,6 +377,9 @@ hipError_t launch_bf16_mma_tiles(const bf16_t* a, const bf16_t* b, const float* 
 // One scaled MFMA per tile (moe_mx_mma_tiles).
 hipError_t launch_mx_mma_tiles(const uint8_t* a, const uint8_t* a_scale, const uint8_t* b, const uint8_t* b_scale,
                                const float* c, float* d, int64_t n, hipStream_t s);
+// One scaled MFMA of E2M1 by E4M3 per tile (moe_mxfp4_mma_tiles).
+hipError_t launch_mxfp4_mma_tiles(const uint8_t* w, const uint8_t* w_scale, const uint8_t* x, const uint8_t* x_scale,
+                                  const float* c, float* d, int64_t n, hipStream_t s);
 // Loads through a buffer address (moe_buffer_reads); lanes a multiple of 64.
 hipError_t launch_buffer_reads(const uint8_t* src, uint32_t length, uint32_t scalar, uint32_t first, int64_t lanes,
                                uint32_t* dst, hipStream_t s);

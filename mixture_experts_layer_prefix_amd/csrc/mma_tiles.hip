@@ -10,11 +10,18 @@
 // K[32+16g, 32+16g+16) in its high 16 bytes, and the scale of row r's K
 // block g.
 //
+// MXFP4 by E4M3 (the routed experts of csrc/routed_ffn.hip): one
+// v_mfma_scale_f32_16x16x128_f8f6f4 per 16x16x128 tile, placed as there: lane
+// l = 16 g + r feeds weight row r with K[32g, 32g+32) and its scale, and token r
+// with K[16g, 16g+16) in its low 16 bytes, K[64+16g, 64+16g+16) in its high ones
+// and the scale of block g.  Accumulator element v of the lane is weight row
+// 4g + v, token r.
+//
 // bf16 (the grouped GEMMs and the router logits of csrc/gemm_bf16.hip): one
 // v_mfma_f32_32x32x16_bf16 per 32x32x16 tile; lane l = 32 g + r feeds row r
 // with K[8g, 8g+8).
 //
-// In both, accumulator element v of lane l is row 4g + 8(v/4) + v%4, column
+// In the 32x32 forms, accumulator element v of lane l is row 4g + 8(v/4) + v%4, column
 // r of the 32x32 result.
 //
 // Beside them the address check of loads through a buffer address, on which
@@ -48,6 +55,30 @@ __global__ __launch_bounds__(64) void mx_mma_tiles_kernel(const uint8_t* __restr
                                                         b_scale[(t * 32 + r) * 2 + g]);
 #pragma unroll
   for (int v = 0; v < 16; ++v) dt[(8 * (v >> 2) + (v & 3)) * 32] = acc[v];
+}
+
+__global__ __launch_bounds__(64) void mxfp4_mma_tiles_kernel(const uint8_t* __restrict__ w,
+                                                             const uint8_t* __restrict__ w_scale,
+                                                             const uint8_t* __restrict__ x,
+                                                             const uint8_t* __restrict__ x_scale,
+                                                             const float* __restrict__ c, float* __restrict__ d) {
+  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x, r = lane & 15, g = lane >> 4;
+  const uint8_t* xr = x + (t * 16 + r) * 128;
+  const u32x4 a = *reinterpret_cast<const u32x4*>(w + (t * 16 + r) * 64 + 16 * g);
+  const u32x4 lo = *reinterpret_cast<const u32x4*>(xr + 16 * g);
+  const u32x4 hi = *reinterpret_cast<const u32x4*>(xr + 64 + 16 * g);
+  const i32x8 fa{(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 fb{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  const float* ct = c + t * 256 + (4 * g) * 16 + r;
+  float* dt = d + t * 256 + (4 * g) * 16 + r;
+  f32x4 acc;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] = ct[v * 16];
+  acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fa, fb, acc, 4, 0, 0, w_scale[(t * 16 + r) * 4 + g], 0,
+                                                         x_scale[(t * 16 + r) * 4 + g]);
+#pragma unroll
+  for (int v = 0; v < 4; ++v) dt[v * 16] = acc[v];
 }
 
 __global__ __launch_bounds__(64) void bf16_mma_tiles_kernel(const bf16_t* __restrict__ a,
@@ -103,6 +134,14 @@ hipError_t launch_bf16_mma_tiles(const bf16_t* a, const bf16_t* b, const float* 
   if (n < 0 || n > INT32_MAX) return hipErrorInvalidValue;
   if (n == 0) return hipSuccess;
   bf16_mma_tiles_kernel<<<(unsigned)n, 64, 0, s>>>(a, b, c, d);
+  return hipGetLastError();
+}
+
+hipError_t launch_mxfp4_mma_tiles(const uint8_t* w, const uint8_t* w_scale, const uint8_t* x, const uint8_t* x_scale,
+                                  const float* c, float* d, int64_t n, hipStream_t s) {
+  if (n < 0 || n > INT32_MAX) return hipErrorInvalidValue;
+  if (n == 0) return hipSuccess;
+  mxfp4_mma_tiles_kernel<<<(unsigned)n, 64, 0, s>>>(w, w_scale, x, x_scale, c, d);
   return hipGetLastError();
 }
 

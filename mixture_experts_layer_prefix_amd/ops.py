@@ -296,6 +296,21 @@ def bf16_mma_tiles(a, b, c):
     return d
 
 
+def mxfp4_mma_tiles(w, w_scale, x, x_scale, c):
+    """moe_mxfp4_mma_tiles: d[t] = c[t] + W[t] X[t]^T per tile through one scaled
+    matrix-core operation of E2M1 by E4M3.  w uint8 [n][16][64] codes, x uint8
+    [n][16][128] E4M3 codes, w_scale and x_scale uint8 [n][16][4] E8M0 codes, c
+    float32 [n][16][16].  Returns d."""
+    n = w.shape[0]
+    assert w.shape == (n, 16, 64) and x.shape == (n, 16, 128) and c.shape == (n, 16, 16)
+    assert w_scale.shape == (n, 16, 4) and x_scale.shape == (n, 16, 4)
+    assert w.dtype == x.dtype == w_scale.dtype == x_scale.dtype == torch.uint8 and c.dtype == torch.float32
+    w, x, w_scale, x_scale, c = (t.contiguous() for t in (w, x, w_scale, x_scale, c))
+    d = torch.empty_like(c)
+    call("moe_mxfp4_mma_tiles", _p(w), _p(w_scale), _p(x), _p(x_scale), _p(c), _p(d), n, _stream())
+    return d
+
+
 def buffer_reads(src, length, scalar, first, lanes):
     """moe_buffer_reads of the uint8 tensor src: int32 (registers [lanes][4],
     LDS [lanes][4], words in registers [lanes], words in LDS [lanes])."""
