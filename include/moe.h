@@ -576,9 +576,11 @@ moe_status moe_clip_grads(const void* const* grads, void* const* out, const int6
  * with max |v| / 2^e <= 6, clamped to [-127, 127] (-127 for an all-zero
  * block); element = v / 2^e rounded to nearest-even E2M1, sign kept; scale
  * byte = e + 127.  dst [rows][cols/2].
- * moe_dequantize_mxfp4: back to bf16, each value once rounded (exact but below
- * bf16's normal numbers), for products with many rows (moe_layer_forward,
- * moe_quantize_mxfp8) from the same weights. */
+ * moe_dequantize_mxfp4: back to bf16, exactly, below bf16's normal numbers too;
+ * a value of 2^128 or more, which bf16 cannot hold, gives infinity (elements of a
+ * block that a finite weight of 1.75 * 2^127 or more leads round to 2^128).  For
+ * products with many rows (moe_layer_forward, moe_quantize_mxfp8) from the same
+ * weights.  A scale byte of 255 (NaN) is outside the contract. */
 moe_status moe_quantize_mxfp4(const void* src_bf16, int64_t rows, int64_t cols, uint8_t* dst, uint8_t* scale,
                               void* stream);
 moe_status moe_dequantize_mxfp4(const uint8_t* src, const uint8_t* scale, int64_t rows, int64_t cols, void* dst_bf16,
