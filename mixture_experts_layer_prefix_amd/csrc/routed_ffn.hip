@@ -78,9 +78,13 @@ __device__ __forceinline__ void in_order() {
 // slabs (256 of K).  Codes: direct loads to LDS of eight rows' whole 128-byte
 // lines, which the streaming hint needs (1.6 GB read so reach 7.0 TB/s, without
 // the hint 6.3; as sixteen rows of half a line with the hint 5.0), and which
-// hold no registers while they are under way.  Without the hint are weights
-// that several workgroups or rounds read, which are to stay in L2 (512 tokens
-// of eight, 32 experts of 7,168 x 2,048: 366 us, all with the hint 440).  A
+// hold no registers while they are under way.  After a schedule, without the
+// hint are weights that several workgroups or rounds read, which are to stay in
+// L2 (512 tokens of eight, 32 experts of 7,168 x 2,048: 366 us, all with the hint
+// 440).  Without a schedule all weights have it: the choice by an expert's tokens
+// gains nothing where they take many rounds and costs the others (64 routes at
+// one of 256 experts of 7,168 x 2,048, 57.1 us, with the choice 56.9, at random
+// ones 202 and 206; 700 at one of 900 of 128 x 256, 123 and 137).  A
 // lane's 16 bytes are put in a place turned by its row, so that the reads of
 // sixteen rows of a slab meet no bank twice.  Scales: a word per row and slab.
 template <int TILES, int STAGES>
@@ -416,10 +420,13 @@ struct Served {
       return true;
     }
   }
-  // The first weights are under way while the tokens are found; but not where
-  // many workgroups find that they have none (16 tokens, 256 experts of 7,168 x
-  // 2,048, k = 8: 380.5 us, always early 389; 2 tokens, 64 of 2,048 x 768, k = 6:
-  // 15.8, early 15.1).
+  // The first weights are under way while the tokens are found; without a
+  // schedule up to sixteen routes only, as of more many workgroups find that they
+  // have none, and have read for nothing (us, after and before the tokens are
+  // found, random experts: 12 routes of 64 of 2,048 x 768, 15.8 and 15.1; 18, 15.0
+  // and 14.8; 30, 19.5 and 19.3; 48, 25.0 and 25.9; 60, 31.6 and 32.8; 24 routes of
+  // 256 of 7,168 x 2,048, 87.3 and 87.6; 64, 206 and 211; 64 of 128 of 4,096 x
+  // 1,536, 93.0 and 98.1; 64 at one of 256 of 7,168 x 2,048, 57.1 and 67.2).
   template <class S, class Issue>
   __device__ __forceinline__ bool start(S& shared, Issue issue) {
     if constexpr (!DIRECT || ALONE) {
