@@ -421,12 +421,15 @@ struct Served {
     }
   }
   // The first weights are under way while the tokens are found; without a
-  // schedule up to sixteen routes only, as of more many workgroups find that they
-  // have none, and have read for nothing (us, after and before the tokens are
-  // found, random experts: 12 routes of 64 of 2,048 x 768, 15.8 and 15.1; 18, 15.0
-  // and 14.8; 30, 19.5 and 19.3; 48, 25.0 and 25.9; 60, 31.6 and 32.8; 24 routes of
-  // 256 of 7,168 x 2,048, 87.3 and 87.6; 64, 206 and 211; 64 of 128 of 4,096 x
-  // 1,536, 93.0 and 98.1; 64 at one of 256 of 7,168 x 2,048, 57.1 and 67.2).
+  // schedule only up to sixteen routes of no fewer experts, as of more many
+  // workgroups find that they have none and have read for nothing.  us, after
+  // and before the tokens are found (routes, experts of d x I, random ids):
+  //   12, 64 of 2,048 x 768       15.8 15.1    24, 256 of 7,168 x 2,048   87.3 87.6
+  //   18                          15.0 14.8    64                         206  211
+  //   30                          19.5 19.3    64, 128 of 4,096 x 1,536   93.0 98.1
+  //   48                          25.0 25.9    32, one a token, 64 of
+  //   60                          31.6 32.8      2,048 x 768              20.8 20.3
+  // 64 routes at one of 256 experts of 7,168 x 2,048: 57.1 and 67.2.
   template <class S, class Issue>
   __device__ __forceinline__ bool start(S& shared, Issue issue) {
     if constexpr (!DIRECT || ALONE) {
